@@ -19,13 +19,18 @@ Four modes, named after the variants on the lesson page "Linear attention and hy
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
 
 import torch
 
 __all__ = ["MODE_ELU1_NORM", "MODE_GATED", "MODE_GATED_DELTA", "MODE_KDA", "MODE_RETNET", "FLAG_INIT_STATE", "LaError",
-           "prefill", "prefill_varlen", "prefill_backward", "prefill_backward_delta", "decode_step", "short_conv", "short_conv_varlen", "short_conv_step", "prefill_conv", "check_status", "library",
+           "prefill", "prefill_varlen", "prefill_backward", "prefill_backward_delta", "decode_step", "short_conv", "short_conv_varlen", "short_conv_step", "prefill_conv",
+           "linear_scan", "linear_scan_varlen", "linear_scan_step", "linear_scan_backward", "rotary",
+           "rotary_step", "rotary_backward", "rotary_frequencies", "rms_norm", "rms_norm_backward",
+           "rms_norm_heads", "rms_norm_heads_backward", "check_status", "library",
            "library_path", "version", "kernel_launches", "workspace_size"]
 
 MODE_ELU1_NORM = 0
@@ -36,6 +41,13 @@ MODE_RETNET = 4
 FLAG_INIT_STATE = 1
 CONV_SILU = 2
 CONV_L2NORM = 4
+SCAN_BLEND = 2
+SCAN_CHECKPOINT = 32   # rows between two states that linear_scan keeps for its backward pass
+ROT_INTERLEAVED = 1
+ROT_TRANSPOSE = 2
+ROT_X_TOKENS = 4
+ROT_Y_TOKENS = 8
+NORM_FP8 = 1
 
 LA_F32 = 0
 LA_BF16 = 1
@@ -108,6 +120,27 @@ def library():
     lib.la_prefill_conv.argtypes = [i, i, i, i, i, i, vp, vp, vp, fp, fp, fp, vp, vp, u, u, vp, fp, fp,
                                     fp, vp, u, vp, ctypes.c_size_t, vp]
     lib.la_prefill_conv.restype = i
+    sz, f = ctypes.c_size_t, ctypes.c_float
+    lib.la_linear_scan.argtypes = [i, i, i, i, vp, fp, fp, vp, fp, u, vp]
+    lib.la_linear_scan.restype = i
+    lib.la_linear_scan_varlen_workspace_size.argtypes = [i]
+    lib.la_linear_scan_varlen_workspace_size.restype = sz
+    lib.la_linear_scan_varlen.argtypes = [i, i, i, i, vp, vp, fp, fp, vp, u, vp, sz, vp]
+    lib.la_linear_scan_varlen.restype = i
+    lib.la_linear_scan_step.argtypes = [i, i, i, vp, fp, fp, vp, u, vp]
+    lib.la_linear_scan_step.restype = i
+    lib.la_linear_scan_backward_workspace_size.argtypes = [i, i, i]
+    lib.la_linear_scan_backward_workspace_size.restype = sz
+    lib.la_linear_scan_backward.argtypes = [i, i, i, i, vp, fp, fp, fp, vp, fp, vp, fp, fp, u, vp, sz, vp]
+    lib.la_linear_scan_backward.restype = i
+    lib.la_rotary.argtypes = [i, i, i, i, i, i, i, vp, vp, vp, vp, i, f, vp, vp, u, vp]
+    lib.la_rotary.restype = i
+    lib.la_rms_norm.argtypes = [i, i, i, i, i, vp, vp, fp, f, vp, vp, fp, i, u, vp]
+    lib.la_rms_norm.restype = i
+    lib.la_rms_norm_backward_workspace_size.argtypes = [i, i, i, i]
+    lib.la_rms_norm_backward_workspace_size.restype = sz
+    lib.la_rms_norm_backward.argtypes = [i, i, i, i, i, vp, fp, f, vp, vp, vp, fp, vp, sz, vp]
+    lib.la_rms_norm_backward.restype = i
     lib.la_selftest_wait_timeout.argtypes = [vp]
     lib.la_selftest_wait_timeout.restype = i
     if hasattr(lib, "la_launch_timing"):   # diagnostic hook, absent from older builds
@@ -609,6 +642,356 @@ def prefill_conv(xq, xk, xv, wq, wk, wv, *, heads: int, beta, gate=None, window=
                                    _stream_handle(xq.device, stream))
     _check(st, "la_prefill_conv")
     return o, state, y, window_out
+
+
+def _int32(**sizes):
+    """Sizes and offsets go to the library as 32-bit ints: refuse what would be cut."""
+    for name, n in sizes.items():
+        if not -2 ** 31 <= n < 2 ** 31:
+            raise ValueError(f"{name}: {n} does not fit in 32 bits")
+
+
+def _on(stream):
+    """Allocations made inside belong to the call's stream."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def linear_scan(x, gate, *, state=None, init_state: bool | None = None, blend: bool = False,
+                checkpoints: bool = False, h=None, stream=None):
+    """Gated linear recurrence with a vector state over whole sequences (``la_linear_scan``):
+    h_t = a_t h_{t-1} + x_t, with ``blend`` a_t h_{t-1} + (1 - a_t) x_t.
+
+    x: [B, T, C] (bf16 or fp32); gate: [B, T, C] fp32, the decays a_t; state: [B, C] fp32 (read
+    as h_0 when ``init_state``, default: when given), overwritten with h_T.  Returns (h [B, T, C],
+    state), and with ``checkpoints`` (the training forward) also the states that
+    ``linear_scan_backward`` starts from, [B, ceil(T / 32), C] fp32.
+    """
+    B, T, C = x.shape
+    _int32(B=B, T=T, C=C)
+    dt = x.dtype
+    dtype = _io_dtype(x)
+    _need(x, (B, T, C), dt, "x")
+    _need(gate, (B, T, C), torch.float32, "gate")
+    if init_state is None:
+        init_state = state is not None
+    if init_state and state is None:
+        raise ValueError("init_state needs a state")
+    with _on(stream):
+        if state is None:
+            state = torch.empty(B, C, device=x.device, dtype=torch.float32)
+        if h is None:
+            h = torch.empty_like(x)
+        kept = (torch.empty(B, -(-T // SCAN_CHECKPOINT), C, device=x.device, dtype=torch.float32)
+                if checkpoints else None)
+    _need(state, (B, C), torch.float32, "state")
+    _need(h, (B, T, C), dt, "h")
+    flags = (FLAG_INIT_STATE if init_state else 0) | (SCAN_BLEND if blend else 0)
+    st = library().la_linear_scan(dtype, B, T, C, _ptr(x), _ptr(gate), _ptr(state), _ptr(h), _ptr(kept),
+                                  flags, _stream_handle(x.device, stream))
+    _check(st, "la_linear_scan")
+    return (h, state, kept) if checkpoints else (h, state)
+
+
+def linear_scan_varlen(x, gate, cu_seqlens, *, state=None, init_state: bool | None = None,
+                       blend: bool = False, h=None, stream=None):
+    """``linear_scan`` of N packed sequences (``la_linear_scan_varlen``): x, gate [T, C] with the
+    sequences back to back, cu_seqlens int32 [N+1] on the device, state [N, C] fp32 (each
+    sequence's start state when ``init_state``, default: when given).  Returns (h [T, C], state)
+    with each sequence's final state in its row.  Rows of no sequence are not written."""
+    T, C = x.shape
+    N = cu_seqlens.numel() - 1
+    if N < 1:
+        raise ValueError("cu_seqlens needs at least two entries")
+    _int32(N=N, T=T, C=C)
+    dt = x.dtype
+    dtype = _io_dtype(x)
+    _need(cu_seqlens, (N + 1,), torch.int32, "cu_seqlens")
+    _need(x, (T, C), dt, "x")
+    _need(gate, (T, C), torch.float32, "gate")
+    if init_state is None:
+        init_state = state is not None
+    if init_state and state is None:
+        raise ValueError("init_state needs a state")
+    nbytes = int(library().la_linear_scan_varlen_workspace_size(T))
+    with _on(stream):
+        if state is None:
+            state = torch.empty(N, C, device=x.device, dtype=torch.float32)
+        if h is None:
+            h = torch.empty_like(x)
+        ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=x.device)
+    _need(state, (N, C), torch.float32, "state")
+    _need(h, (T, C), dt, "h")
+    flags = (FLAG_INIT_STATE if init_state else 0) | (SCAN_BLEND if blend else 0)
+    st = library().la_linear_scan_varlen(dtype, N, T, C, _ptr(cu_seqlens), _ptr(x), _ptr(gate), _ptr(state),
+                                         _ptr(h), flags, _ptr(ws), ws.numel(),
+                                         _stream_handle(x.device, stream))
+    _check(st, "la_linear_scan_varlen")
+    return h, state
+
+
+def linear_scan_step(x, gate, state, *, blend: bool = False, h=None, stream=None):
+    """One new token of N sequences (``la_linear_scan_step``): x [N, C], gate [N, C] fp32, state
+    [N, C] fp32 updated in place.  Returns h [N, C]."""
+    N, C = x.shape
+    _int32(N=N, C=C)
+    dt = x.dtype
+    dtype = _io_dtype(x)
+    _need(x, (N, C), dt, "x")
+    _need(gate, (N, C), torch.float32, "gate")
+    _need(state, (N, C), torch.float32, "state")
+    if h is None:
+        with _on(stream):
+            h = torch.empty_like(x)
+    _need(h, (N, C), dt, "h")
+    st = library().la_linear_scan_step(dtype, N, C, _ptr(x), _ptr(gate), _ptr(state), _ptr(h),
+                                       SCAN_BLEND if blend else 0, _stream_handle(x.device, stream))
+    _check(st, "la_linear_scan_step")
+    return h
+
+
+def linear_scan_backward(x, gate, dh, *, state0=None, checkpoints=None, dstate=None, blend: bool = False,
+                         need_dgate: bool = True, need_dstate0: bool | None = None, stream=None):
+    """Gradients of ``linear_scan`` (``la_linear_scan_backward``).
+
+    x, dh: [B, T, C]; gate: [B, T, C] fp32; checkpoints: what ``linear_scan`` kept for the same
+    inputs (None: formed again from state0 [B, C], None: zeros); dstate: [B, C] fp32, the
+    gradient of the final state, or None.  Returns (dx, dgate, dstate0): dgate [B, T, C] fp32
+    when ``need_dgate``, dstate0 [B, C] when ``need_dstate0`` (default: when state0 is given).
+    """
+    B, T, C = x.shape
+    _int32(B=B, T=T, C=C)
+    dt = x.dtype
+    dtype = _io_dtype(x)
+    _need(x, (B, T, C), dt, "x")
+    _need(dh, (B, T, C), dt, "dh")
+    _need(gate, (B, T, C), torch.float32, "gate")
+    for name, t in (("state0", state0), ("dstate", dstate)):
+        if t is not None:
+            _need(t, (B, C), torch.float32, name)
+    if checkpoints is not None:
+        _need(checkpoints, (B, -(-T // SCAN_CHECKPOINT), C), torch.float32, "checkpoints")
+    if need_dstate0 is None:
+        need_dstate0 = state0 is not None
+    nbytes = 0 if checkpoints is not None else int(library().la_linear_scan_backward_workspace_size(B, T, C))
+    with _on(stream):
+        dx = torch.empty_like(x)
+        dgate = torch.empty_like(gate) if need_dgate else None
+        dstate0 = torch.empty(B, C, device=x.device, dtype=torch.float32) if need_dstate0 else None
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device) if nbytes else None
+    st = library().la_linear_scan_backward(dtype, B, T, C, _ptr(x), _ptr(gate), _ptr(state0), _ptr(checkpoints),
+                                           _ptr(dh), _ptr(dstate), _ptr(dx), _ptr(dgate), _ptr(dstate0),
+                                           SCAN_BLEND if blend else 0, _ptr(ws), nbytes,
+                                           _stream_handle(x.device, stream))
+    _check(st, "la_linear_scan_backward")
+    return dx, dgate, dstate0
+
+
+def rotary_frequencies(rotary_dim: int, *, base: float = 10000.0, scaling: str | None = None,
+                       factor: float = 1.0, original_length: int | None = None, device="cuda"):
+    """The angles per position of ``rotary`` and the factor on the turned values.
+
+    theta_j = base^(-2j / rotary_dim), j < rotary_dim / 2, in fp64.  ``scaling`` stretches them for
+    contexts ``factor`` times as long: "linear" divides every angle (position interpolation);
+    "ntk" enlarges the base to base * factor^(r / (r - 2)), so that the slowest pair is divided by
+    the factor and the fastest left alone; "yarn" divides the pairs that turn less than once over
+    ``original_length``, leaves those that turn more than 32 times, blends in between, and
+    enlarges the values by 0.1 ln(factor) + 1.  Returns (freqs [rotary_dim / 2] fp64, scale).
+    """
+    if rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be even and at least 2")
+    if not base > 0 or not factor > 0:
+        raise ValueError("base and factor must be positive")
+    j = torch.arange(rotary_dim // 2, dtype=torch.float64)
+    scale = 1.0
+    if scaling == "ntk":
+        if rotary_dim < 4:
+            raise ValueError("ntk scaling needs rotary_dim >= 4")
+        base = base * factor ** (rotary_dim / (rotary_dim - 2))
+    freqs = base ** (-2.0 * j / rotary_dim)
+    if scaling == "linear":
+        freqs = freqs / factor
+    elif scaling == "yarn":
+        if not original_length or original_length < 1:
+            raise ValueError("yarn scaling needs original_length")
+        turns = freqs * (original_length / (2.0 * math.pi))
+        keep = ((turns - 1.0) / 31.0).clamp(0.0, 1.0)
+        freqs = freqs * (keep + (1.0 - keep) / factor)
+        scale = 0.1 * math.log(factor) + 1.0 if factor > 1.0 else 1.0
+    elif scaling not in (None, "ntk"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return freqs.to(device), scale
+
+
+def _rotary_sizes(t, d, name):
+    """(token-major, B, T, H, d) of a [B, T, H*d] or [B, H, T, d] tensor."""
+    if t.dim() == 3:
+        if not d or t.shape[2] % d:
+            raise ValueError(f"{name}: a token-major tensor needs d, a divisor of its last dimension")
+        return True, t.shape[0], t.shape[1], t.shape[2] // d, d
+    if t.dim() != 4:
+        raise ValueError(f"{name}: expected [B, T, H*d] or [B, H, T, d], got {tuple(t.shape)}")
+    if d is not None and d != t.shape[3]:
+        raise ValueError(f"{name}: d is {t.shape[3]}, not {d}")
+    return False, t.shape[0], t.shape[2], t.shape[1], t.shape[3]
+
+
+def _rotary(q, k, freqs, d, positions, start, scale, interleaved, transpose, y_tokens, in_place, stream):
+    dt = q.dtype
+    dtype = _io_dtype(q)
+    x_tokens, B, T, Hq, d = _rotary_sizes(q, d, "q")
+    _need(q, q.shape, dt, "q")
+    Hk = 0
+    if k is not None:
+        kt, kB, kT, Hk, _ = _rotary_sizes(k, d, "k")
+        if (kt, kB, kT) != (x_tokens, B, T):
+            raise ValueError(f"k: expected q's layout, batch and length, got {tuple(k.shape)}")
+        _need(k, k.shape, dt, "k")
+    _int32(B=B, T=T, start=int(start))
+    _need(freqs, (freqs.numel(),), torch.float64, "freqs")
+    if positions is not None:
+        _need(positions, (B, T), torch.int32, "positions")
+    if in_place:
+        if x_tokens != y_tokens:
+            raise ValueError("in_place keeps the layout")
+        yq, yk = q, k
+    else:
+        def out(H):
+            return torch.empty((B, T, H * d) if y_tokens else (B, H, T, d), device=q.device, dtype=dt)
+        with _on(stream):
+            yq, yk = out(Hq), (out(Hk) if Hk else None)
+    flags = ((ROT_INTERLEAVED if interleaved else 0) | (ROT_TRANSPOSE if transpose else 0)
+             | (ROT_X_TOKENS if x_tokens else 0) | (ROT_Y_TOKENS if y_tokens else 0))
+    st = library().la_rotary(dtype, B, T, Hq, Hk, d, 2 * freqs.numel(), _ptr(q), _ptr(k), _ptr(freqs),
+                             _ptr(positions), int(start), float(scale), _ptr(yq), _ptr(yk), flags,
+                             _stream_handle(q.device, stream))
+    _check(st, "la_rotary")
+    return yq if k is None else (yq, yk)
+
+
+def rotary(q, k=None, *, freqs, d: int | None = None, positions=None, start: int = 0, scale: float = 1.0,
+           interleaved: bool = False, in_place: bool = False, stream=None):
+    """Rotary positions of q and k (``la_rotary``), head-major out: the q and k of ``prefill``.
+
+    q, k: [B, T, H*d] token-major (a projection's output, with ``d``) or [B, H, T, d]; k may have
+    another number of heads, or be None.  freqs: fp64 [r / 2] (``rotary_frequencies``): the first r
+    values of each head turn, in pairs (x_j, x_{j + r/2}), with ``interleaved`` (x_2j, x_2j+1).
+    positions: int32 [B, T], or None: start + t; packed sequences are B = 1 with positions.
+    ``in_place`` (head-major inputs) turns q and k where they lie.  Returns y_q, or (y_q, y_k).
+    """
+    return _rotary(q, k, freqs, d, positions, start, scale, interleaved, False, False, in_place, stream)
+
+
+def rotary_step(q, k=None, *, freqs, d: int, positions, scale: float = 1.0, interleaved: bool = False,
+                stream=None):
+    """One new token of N sequences: q [N, H*d], k [N, H_k*d], positions int32 [N].  Returns y_q
+    [N, H, d] (the q of ``decode_step``), or (y_q, y_k)."""
+    if q.dim() != 2 or (k is not None and k.dim() != 2):
+        raise ValueError("q and k must be [N, H*d]")
+    _need(positions, (q.shape[0],), torch.int32, "positions")
+    y = _rotary(q.unsqueeze(1), None if k is None else k.unsqueeze(1), freqs, d, positions.unsqueeze(1), 0,
+                scale, interleaved, False, False, False, stream)
+    return y.squeeze(2) if k is None else (y[0].squeeze(2), y[1].squeeze(2))
+
+
+def rotary_backward(dq, dk=None, *, freqs, d: int | None = None, positions=None, start: int = 0,
+                    scale: float = 1.0, interleaved: bool = False, token_major: bool = False,
+                    in_place: bool = False, stream=None):
+    """Gradients of ``rotary`` (the transposed rotation): dq, dk [B, H, T, d] (or [B, T, H*d] with
+    ``d``), the other arguments as for ``rotary``.  Returns the gradients of q and k, head-major or
+    (``token_major``) [B, T, H*d] as the projections gave them."""
+    return _rotary(dq, dk, freqs, d, positions, start, scale, interleaved, True, token_major, in_place, stream)
+
+
+def _rms_norm(x, B, H, T, C, w, residual, residual_out, eps, fp8, group, y_shape, scale_shape, stream):
+    dt = x.dtype
+    dtype = _io_dtype(x)
+    _need(x, x.shape, dt, "x")
+    _need(w, (C,), torch.float32, "w")
+    if group and not fp8:
+        raise ValueError("group needs fp8")
+    if residual is not None:
+        _need(residual, x.shape, dt, "residual")
+    elif residual_out is not None:
+        raise ValueError("residual_out needs residual")
+    _int32(B=B, H=H, rows=T, C=C)
+    with _on(stream):
+        y = torch.empty(y_shape, device=x.device, dtype=torch.float8_e4m3fn if fp8 else dt)
+        scales = torch.empty(scale_shape, device=x.device, dtype=torch.float32) if fp8 else None
+        if residual is not None and residual_out is None:
+            residual_out = torch.empty_like(x)
+    if residual is not None:
+        _need(residual_out, x.shape, dt, "residual_out")
+    st = library().la_rms_norm(dtype, B, H, T, C, _ptr(x), _ptr(residual), _ptr(w), float(eps),
+                               _ptr(residual_out), _ptr(y), _ptr(scales), int(group),
+                               NORM_FP8 if fp8 else 0, _stream_handle(x.device, stream))
+    _check(st, "la_rms_norm")
+    out = (y,) + ((scales,) if fp8 else ()) + ((residual_out,) if residual is not None else ())
+    return out[0] if len(out) == 1 else out
+
+
+def _rows(x):
+    n = 1
+    for s in x.shape[:-1]:
+        n *= s
+    return n
+
+
+def rms_norm(x, w, *, residual=None, residual_out=None, eps: float = 1e-6, fp8: bool = False, group: int = 0,
+             stream=None):
+    """Root-mean-square norm of the last dimension, with the residual's addition (``la_rms_norm``).
+
+    x, residual: [.., C] (bf16 or fp32); w: [C] fp32.  h = x + residual (rounded as it is stored),
+    y = h / sqrt(mean(h^2) + eps) * w.  ``fp8``: y leaves as e4m3 with fp32 scales, one a row
+    (``group`` 0) or one for each 128 columns (``group`` 128); y = q * scale.  Returns y, or (q,
+    scales [.., C / group]), with a residual followed by h (``residual_out``, which may be residual
+    itself).
+    """
+    C = x.shape[-1]
+    if group and C % group:
+        raise ValueError("group must divide the last dimension")
+    return _rms_norm(x, 1, 1, _rows(x), C, w, residual, residual_out, eps, fp8, group, x.shape,
+                     (*x.shape[:-1], C // group if group else 1), stream)
+
+
+def rms_norm_heads(x, w, *, eps: float = 1e-6, fp8: bool = False, stream=None):
+    """The norm after the attention: every head's row of x [B, H, T, d] (the o of ``prefill``), w [d]
+    fp32; the rows leave token-major, [B, T, H*d], for the output projection.  ``fp8``: returns
+    (q [B, T, H*d] e4m3, scales [B, T, H]), one scale for each head's row."""
+    B, H, T, d = x.shape
+    return _rms_norm(x, B, H, T, d, w, None, None, eps, fp8, 0, (B, T, H * d), (B, T, H), stream)
+
+
+def _rms_norm_backward(h, B, H, T, C, w, dy, dy_shape, dresidual, eps, stream):
+    dt = h.dtype
+    dtype = _io_dtype(h)
+    _need(h, h.shape, dt, "h")
+    _need(w, (C,), torch.float32, "w")
+    _need(dy, dy_shape, dt, "dy")
+    if dresidual is not None:
+        _need(dresidual, h.shape, dt, "dresidual")
+    _int32(B=B, H=H, rows=T, C=C)
+    nbytes = int(library().la_rms_norm_backward_workspace_size(B, H, T, C))
+    with _on(stream):
+        dx, dw = torch.empty_like(h), torch.empty_like(w)
+        ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=h.device)
+    st = library().la_rms_norm_backward(dtype, B, H, T, C, _ptr(h), _ptr(w), float(eps), _ptr(dy),
+                                        _ptr(dresidual), _ptr(dx), _ptr(dw), _ptr(ws), ws.numel(),
+                                        _stream_handle(h.device, stream))
+    _check(st, "la_rms_norm_backward")
+    return dx, dw
+
+
+def rms_norm_backward(h, w, dy, *, dresidual=None, eps: float = 1e-6, stream=None):
+    """Gradients of ``rms_norm`` (``la_rms_norm_backward``): h [.., C] the stored stream (x itself
+    without a residual), dy [.., C], dresidual [.., C] the stream's gradient from elsewhere or
+    None.  Returns (dx, dw): dx is the gradient of x and of residual alike, dw [C] fp32."""
+    return _rms_norm_backward(h, 1, 1, _rows(h), h.shape[-1], w, dy, h.shape, dresidual, eps, stream)
+
+
+def rms_norm_heads_backward(x, w, dy, *, eps: float = 1e-6, stream=None):
+    """Gradients of ``rms_norm_heads``: x [B, H, T, d], dy [B, T, H*d].  Returns (dx, dw)."""
+    B, H, T, d = x.shape
+    return _rms_norm_backward(x, B, H, T, d, w, dy, (B, T, H * d), None, eps, stream)
 
 
 def selftest_wait_timeout(stream=None):

@@ -369,6 +369,164 @@ la_status_t la_prefill_backward_delta(la_mode_t mode, la_dtype_t dtype, int B, i
                                       float *dstate0, void *workspace, size_t workspace_bytes,
                                       void *stream);
 
+/* Flag of the la_linear_scan* entry points: u_t = (1 - a_t) x_t instead of x_t. */
+#define LA_SCAN_BLEND 2u
+
+/*
+ * la_linear_scan -- the gated linear recurrence with a vector state: the decayed memory of
+ * [decay/gates] with one number per channel instead of a matrix per head.  Per batch row and
+ * channel,
+ *
+ *   h_t = a_t h_{t-1} + u_t,   u_t = x_t, or (1 - a_t) x_t with LA_SCAN_BLEND,
+ *
+ * as a scan over the whole sequence (the time axis is split over threads, warps and the
+ * CTAs of a cluster and joined exactly; the same bits on every call).  The pages fix only the
+ * decayed update; the vector state and the blend are this library's reading.
+ *
+ *   x           [B, T, C]  I/O dtype, token-major (a projection's output)
+ *   gate        [B, T, C]  fp32 decay values a_t (required)
+ *   state       [B, C]     fp32, in (with LA_FLAG_INIT_STATE: h_0, else zeros) and out: h_T
+ *   h           [B, T, C]  I/O dtype, out (one rounding of the fp32 state)
+ *   checkpoints [B, ceil(T / 32), C] fp32, out, or NULL: the state in front of every 32nd row
+ *               (row 0: h_0), for la_linear_scan_backward
+ *   flags       LA_FLAG_INIT_STATE | LA_SCAN_BLEND
+ * Any C >= 1, and tensors may start at any element (a row of a larger one): C a multiple of 4
+ * with 16-byte starts takes four channels a thread, else two or, slowest, one.  T = 0 leaves or
+ * zeroes the state.  No output may overlap an input or another output.
+ */
+la_status_t la_linear_scan(la_dtype_t dtype, int B, int T, int C, const void *x, const float *gate,
+                           float *state, void *h, float *checkpoints, unsigned flags, void *stream);
+
+/*
+ * la_linear_scan_varlen -- la_linear_scan over N packed sequences, each with its own state;
+ * nothing (no NaN either) crosses from one sequence into the next.
+ *   cu_seqlens  [N + 1] int32, DEVICE memory, as for la_prefill_varlen (entries outside
+ *               [0, T] or decreasing are reported by la_check_status())
+ *   x, gate, h  [T, C]; rows of no sequence (before cu_seqlens[0], from cu_seqlens[N] on) are
+ *               left as they were in h
+ *   state       [N, C] fp32 in (with LA_FLAG_INIT_STATE) and out; an empty sequence keeps its
+ *               state (without the flag: zeros)
+ *   workspace   at least la_linear_scan_varlen_workspace_size(T) bytes (the sequence of every
+ *               row), 16-byte aligned; required for T > 0
+ * Two launches: the rows' sequences and the check of the offsets, then the scan.
+ */
+size_t la_linear_scan_varlen_workspace_size(int T);
+la_status_t la_linear_scan_varlen(la_dtype_t dtype, int N, int T, int C, const int *cu_seqlens,
+                                  const void *x, const float *gate, float *state, void *h,
+                                  unsigned flags, void *workspace, size_t workspace_bytes,
+                                  void *stream);
+
+/*
+ * la_linear_scan_step -- one new token of N sequences: x, h [N, C], gate [N, C] fp32, state
+ * [N, C] fp32 updated in place; flags 0 or LA_SCAN_BLEND.
+ */
+la_status_t la_linear_scan_step(la_dtype_t dtype, int N, int C, const void *x, const float *gate,
+                                float *state, void *h, unsigned flags, void *stream);
+
+/*
+ * la_linear_scan_backward -- gradients of la_linear_scan for L = sum_t dh_t . h_t +
+ * dstate . h_T: with l_t = dh_t + a_{t+1} l_{t+1} (l_T = dh_T + dstate),
+ *   dx_t = l_t,  da_t = l_t h_{t-1},  dh_0 = a_1 l_1
+ * (LA_SCAN_BLEND: dx_t = (1 - a_t) l_t, da_t = l_t (h_{t-1} - x_t)).  The states h_{t-1} are
+ * fp32, walked again from the checkpoints.
+ *
+ *   x, gate, flags   as given to la_linear_scan (without LA_FLAG_INIT_STATE)
+ *   checkpoints      what la_linear_scan kept for these inputs, or NULL: formed by one more
+ *                    forward pass from state0, in the workspace
+ *   state0           [B, C] fp32 h_0, or NULL (zeros); read only without checkpoints
+ *   dh               [B, T, C] I/O dtype       dstate [B, C] fp32, or NULL (zeros)
+ *   dx               out [B, T, C] I/O dtype   dgate out [B, T, C] fp32, or NULL
+ *   dstate0          out [B, C] fp32, or NULL
+ *   workspace        at least la_linear_scan_backward_workspace_size() bytes without
+ *                    checkpoints (else unused, may be NULL)
+ * T >= 1.  Element alignment (workspace 16); no output or workspace may overlap an input or one
+ * another.
+ */
+size_t la_linear_scan_backward_workspace_size(int B, int T, int C);
+la_status_t la_linear_scan_backward(la_dtype_t dtype, int B, int T, int C, const void *x,
+                                    const float *gate, const float *state0,
+                                    const float *checkpoints, const void *dh, const float *dstate,
+                                    void *dx, float *dgate, float *dstate0, unsigned flags,
+                                    void *workspace, size_t workspace_bytes, void *stream);
+
+/* Flags of la_rotary. */
+#define LA_ROT_INTERLEAVED 1u   /* pairs (x_2j, x_2j+1); without it (x_j, x_{j + r/2}) */
+#define LA_ROT_TRANSPOSE 2u     /* the transposed rotation: the gradient */
+#define LA_ROT_X_TOKENS 4u      /* q, k are [B, T, H*d]; without it [B, H, T, d] */
+#define LA_ROT_Y_TOKENS 8u      /* y_q, y_k are [B, T, H*d]; without it [B, H, T, d] */
+
+/*
+ * la_rotary -- rotary positions of q and k: the first r = rotary_dim values of every head row
+ * turn in pairs (u, v) by angle = position * freqs[j], j < r / 2,
+ *   u' = scale (u cos - v sin),   v' = scale (u sin + v cos),
+ * and the other d - r pass through.  It stands in front of the constant-decay prefill
+ * ([decay/gates]) and of the softmax layers of hybrids; with LA_ROT_X_TOKENS it takes a
+ * projection's rows to the head-major q and k of la_prefill and la_decode_step, as
+ * la_short_conv does.  The pages do not give it: the formula is this library's reading.
+ *
+ *   q, y_q     H_q heads, I/O dtype      k, y_k   H_k heads (0: none, k and y_k ignored)
+ *   freqs      [rotary_dim / 2] fp64 angles per position, any scaling for long contexts
+ *              already in them; angles are formed and reduced in fp64
+ *   positions  [B, T] int32, or NULL: start + t
+ *   scale      factor on the turned values (1 for a plain rotation)
+ *   rotary_dim even, 2 .. d; d <= 512 (LA_ERR_UNSUPPORTED above).  Rows whose d is a multiple
+ *              of 8 and rotary_dim of 16 move in 16-byte vectors, others singly.
+ * T >= 0.  Decoding is T = 1 with positions; packed sequences are B = 1 with positions.
+ * 16-byte alignment (freqs 8, positions 4).  y_q may be q (and y_k k) where the layouts
+ * agree; any other overlap is LA_ERR_INVALID_ARG.
+ */
+la_status_t la_rotary(la_dtype_t dtype, int B, int T, int H_q, int H_k, int d, int rotary_dim,
+                      const void *q, const void *k, const double *freqs, const int *positions,
+                      int start, float scale, void *y_q, void *y_k, unsigned flags, void *stream);
+
+/* Flag of la_rms_norm: 8-bit output. */
+#define LA_NORM_FP8 1u
+
+/*
+ * la_rms_norm -- the root-mean-square norm of rows of C values, with the residual's addition:
+ *   h = x + residual (rounded to the I/O dtype; without residual h = x),
+ *   y = h / sqrt(mean(h^2) + eps) * w,
+ * after the attention ([decay/gates]: modern variants drop the denominator and normalise
+ * there), where rows of one head go from head-major to token-major, and in front of a layer's
+ * projections.  The norm's formula is this library's reading.
+ *
+ *   x             [B, H, T, C] I/O dtype (plain rows: B = H = 1)
+ *   residual      [B, T, C] I/O dtype, H = 1 only, or NULL
+ *   w             [C] fp32          eps  >= 0
+ *   residual_out  [B, T, C] out: h (required with residual; may be residual or x itself)
+ *   y             [B, T, H, C] out, I/O dtype; with LA_NORM_FP8 e4m3 bytes q = y / scale,
+ *                 round to nearest even, saturating
+ *   scales        [B, T, H, C / group] fp32 out with LA_NORM_FP8 (ignored without): max |y| /
+ *                 448 over `group` columns (at least 2^-126; 1 where all are zero)
+ *   group         0 (a scale for the whole row) or 128 (C a multiple of 128)
+ * C <= 16384 (LA_ERR_UNSUPPORTED above); multiples of 8 take 16-byte vectors.  T = 0 does
+ * nothing.  A row with an infinity or a NaN gives NaN at least there.  16-byte alignment
+ * (scales 4); any overlap but those named is LA_ERR_INVALID_ARG.
+ */
+la_status_t la_rms_norm(la_dtype_t dtype, int B, int H, int T, int C, const void *x,
+                        const void *residual, const float *w, float eps, void *residual_out,
+                        void *y, float *scales, int group, unsigned flags, void *stream);
+
+/*
+ * la_rms_norm_backward -- gradients of la_rms_norm (I/O-dtype output): with n = h rstd and
+ * p = dy w, dx = rstd (p - n mean(p n)) + dresidual and dw = sum over rows of dy n.  dx is
+ * the gradient of x and of residual alike.
+ *   h          [B, H, T, C] I/O dtype: the stored stream (without residual: x)
+ *   dy         [B, T, H, C] I/O dtype
+ *   dresidual  [B, H, T, C] I/O dtype: the gradient of the stored stream from elsewhere, or
+ *              NULL (zeros)
+ *   dx         out [B, H, T, C] I/O dtype       dw  out [C] fp32
+ *   workspace  at least la_rms_norm_backward_workspace_size() bytes (partial sums of dw, added
+ *              in a fixed order)
+ * T = 0 zeroes dw.  16-byte alignment; no output or workspace may overlap anything.  Two
+ * launches.
+ */
+size_t la_rms_norm_backward_workspace_size(int B, int H, int T, int C);
+la_status_t la_rms_norm_backward(la_dtype_t dtype, int B, int H, int T, int C, const void *h,
+                                 const float *w, float eps, const void *dy, const void *dresidual,
+                                 void *dx, float *dw, void *workspace, size_t workspace_bytes,
+                                 void *stream);
+
 /*
  * la_check_status -- synchronise `stream`, then report the first device-side failure
  * since the last call: LA_ERR_CUDA for a CUDA error, LA_ERR_TIMEOUT if a kernel's
@@ -401,7 +559,7 @@ unsigned long long la_kernel_launches(void);
 /* Per-launch device timing, a measurement aid with no counterpart in the pages.
  * la_launch_timing(1) makes every later call of la_prefill, la_prefill_noalloc,
  * la_prefill_varlen, la_prefill_backward, la_prefill_backward_delta, la_decode_step and
- * the la_short_conv* entry
+ * the la_short_conv*, la_linear_scan*, la_rotary and la_rms_norm* entry
  * points bracket each
  * kernel it enqueues
  * with two CUDA events recorded on the call's stream (at most 16 launches per call are
