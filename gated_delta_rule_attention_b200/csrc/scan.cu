@@ -32,6 +32,7 @@
 // the backward pass too reads each input once.
 #include "la_internal.cuh"
 #include "ptx.cuh"
+#include "tmap.cuh"
 #include "vec.cuh"
 
 #include <atomic>
@@ -656,6 +657,525 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(const Backwa
     }
 }
 
+// ------------------------------------------------------------------------------- rows by TMA
+
+// V neighbouring channels of one lane, as one (V = 1) or packed (V = 2) fp32 operand.
+template <int V>
+struct Lane;
+template <>
+struct Lane<1> {
+    float v;
+    static __device__ __forceinline__ Lane all(float x) { return {x}; }
+    __device__ __forceinline__ float get(int) const { return v; }
+    __device__ __forceinline__ void set(int, float x) { v = x; }
+    static __device__ __forceinline__ Lane load(const float *p) { return {*p}; }
+    static __device__ __forceinline__ Lane load(const __nv_bfloat16 *p) { return {__bfloat162float(*p)}; }
+    __device__ __forceinline__ void store(float *p) const { *p = v; }
+    __device__ __forceinline__ void store(__nv_bfloat16 *p) const { *p = __float2bfloat16_rn(v); }
+};
+template <>
+struct Lane<2> {
+    unsigned long long v;
+    static __device__ __forceinline__ Lane make(float a, float b) {
+        Lane r;
+        asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+        return r;
+    }
+    static __device__ __forceinline__ Lane all(float x) { return make(x, x); }
+    __device__ __forceinline__ float2 both() const {
+        float2 r;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+        return r;
+    }
+    __device__ __forceinline__ float get(int j) const { return j ? both().y : both().x; }
+    __device__ __forceinline__ void set(int j, float x) {
+        const float2 b = both();
+        *this = j ? make(b.x, x) : make(x, b.y);
+    }
+    static __device__ __forceinline__ Lane load(const float *p) {
+        const float2 f = *reinterpret_cast<const float2 *>(p);
+        return make(f.x, f.y);
+    }
+    static __device__ __forceinline__ Lane load(const __nv_bfloat16 *p) {
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(p);   // bf16 -> fp32: the high half
+        return make(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
+    __device__ __forceinline__ void store(float *p) const { *reinterpret_cast<float2 *>(p) = both(); }
+    __device__ __forceinline__ void store(__nv_bfloat16 *p) const {
+        const float2 f = both();
+        *reinterpret_cast<uint32_t *>(p) = ptx::pack_bf16x2(f.x, f.y);
+    }
+};
+__device__ __forceinline__ Lane<1> fma(Lane<1> a, Lane<1> b, Lane<1> c) { return {fmaf(a.v, b.v, c.v)}; }
+__device__ __forceinline__ Lane<1> mul(Lane<1> a, Lane<1> b) { return {a.v * b.v}; }
+__device__ __forceinline__ Lane<1> add(Lane<1> a, Lane<1> b) { return {a.v + b.v}; }
+__device__ __forceinline__ Lane<2> fma(Lane<2> a, Lane<2> b, Lane<2> c) {
+    Lane<2> r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ Lane<2> mul(Lane<2> a, Lane<2> b) {
+    Lane<2> r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ Lane<2> add(Lane<2> a, Lane<2> b) {
+    Lane<2> r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+// (1 - a) x with one rounding of the exact x - a x
+template <int V>
+__device__ __forceinline__ Lane<V> blended(Lane<V> a, Lane<V> x) {
+    return fma(mul(a, Lane<V>::all(-1.f)), x, x);
+}
+
+// (P, H) of a run of rows, one lane's channels.
+template <int V>
+struct alignas(8 * V) Run {
+    Lane<V> P, H;
+};
+// To shared memory of CTA `rank` of the cluster; the bytes count towards its barrier `bar` (both
+// given by this CTA's own addresses).
+__device__ __forceinline__ uint32_t of_rank(uint32_t addr, uint32_t rank) {
+    uint32_t to;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(addr), "r"(rank));
+    return to;
+}
+__device__ __forceinline__ void send(uint32_t addr, uint32_t bar, uint32_t rank, const Run<1> &r) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(
+                     of_rank(addr, rank)),
+                 "f"(r.P.v), "f"(r.H.v), "r"(of_rank(bar, rank))
+                 : "memory");
+}
+__device__ __forceinline__ void send(uint32_t addr, uint32_t bar, uint32_t rank, const Run<2> &r) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b64 [%0], {%1, %2}, [%3];" ::"r"(
+                     of_rank(addr, rank)),
+                 "l"(r.P.v), "l"(r.H.v), "r"(of_rank(bar, rank))
+                 : "memory");
+}
+__device__ __forceinline__ void send(uint32_t addr, uint32_t bar, uint32_t rank, int v) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.s32 [%0], %1, [%2];" ::"r"(of_rank(addr, rank)),
+                 "r"(v), "r"(of_rank(bar, rank))
+                 : "memory");
+}
+
+struct TmaScanParams {
+    CUtensorMap gate, x;     // [B][T][C], boxes of S rows x 32 V channels
+    ScanParams s;
+    unsigned *err;
+};
+
+// After a wait that ran out: give the copies still in flight 10 ms to land before the block's
+// shared memory goes.
+__device__ __noinline__ void settle() {
+    for (int i = 0; i < 1000; ++i) __nanosleep(10000);
+}
+
+// Shape: V channels a lane, E elements a thread; a warp has S rows of 32 V channels.
+template <int V_, int E_>
+struct TmaShape {
+    static constexpr int V = V_, E = E_, S = E / V, CH = 32 * V, TT = kWarps * S;
+};
+
+// Shared memory: the ring, [STAGES][kWarps] of (gate rows, x rows); then this.
+template <typename SH, int STAGES>
+struct TmaExchange {
+    Run<SH::V> warp[2][kWarps][32];   // by the step's parity
+    uint64_t full[STAGES][kWarps];
+    uint64_t met[2];                  // K > 1: the step's runs of all ranks are here
+    int reset[2][kWarps];
+    int slot_reset[2][kMaxCluster];
+    int abort;
+    // followed, on 16 bytes, by Run slot[2][K][32]
+};
+template <typename IO, typename SH>
+constexpr uint32_t tma_rows_bytes() { return SH::S * SH::CH * (sizeof(float) + sizeof(IO)); }
+
+// Each warp runs its own pipeline: one lane asks for the boxes of the warp's rows, STAGES steps
+// ahead, into a part of the ring that only this warp reads.  All lanes of a warp hold the same
+// rows, so rows behind the end, sequence starts and full tiles are decided for the whole warp.
+// Every thread folds the eight warps' (P, H) of its channels itself, and with K > 1 the K
+// CTAs', so a step has one barrier of the CTA and no thread waits for another's fold.  With K > 1
+// the ranks' runs are sent to each other by st.async, whose bytes complete the receiver's
+// barrier of the step's parity.  A slot is written again two steps later: its sender has then
+// had this CTA's run of the step between, sent after all of this CTA had read the slot.
+template <typename IO, typename SH, int STAGES, bool BLEND, bool PACKED>
+__global__ void __launch_bounds__(kThreads, 2) scan_tma_kernel(const __grid_constant__ TmaScanParams q) {
+    constexpr int V = SH::V, S = SH::S, CH = SH::CH, TT = SH::TT;
+    constexpr uint32_t kRows = tma_rows_bytes<IO, SH>();
+    using L = Lane<V>;
+    extern __shared__ __align__(128) unsigned char boxes[];
+    auto *ex = reinterpret_cast<TmaExchange<SH, STAGES> *>(boxes + (size_t)STAGES * kWarps * kRows);
+    auto *slots = reinterpret_cast<Run<V> *>(boxes + (size_t)STAGES * kWarps * kRows +
+                                             (sizeof(TmaExchange<SH, STAGES>) + 15) / 16 * 16);
+    const ScanParams &p = q.s;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int K = p.K, rank = blockIdx.x % K;
+    const long long col = blockIdx.x / K;
+    const int b = (int)(col / p.blocks);
+    const int cb = (int)(col % p.blocks) * CH, c0 = cb + lane * V;
+    const bool act = c0 < p.C;
+    const long long T = p.T, C = p.C;
+    IO *hb = p.h ? static_cast<IO *>(p.h) + b * T * C + c0 : nullptr;
+
+    if (tid < STAGES * kWarps) ptx::mbar_init(&ex->full[0][0] + tid, 1);
+    if (tid == 0) {
+        ex->abort = 0;
+        ptx::mbar_init(&ex->met[0], 1);
+        ptx::mbar_init(&ex->met[1], 1);
+    }
+    ptx::fence_mbar_init();
+    if (K > 1) {   // also: every CTA of the cluster runs before the first store to its shared memory
+        cluster_arrive();
+        cluster_wait();
+    } else {
+        __syncthreads();
+    }
+    auto first_row = [&](int step) { return ((long long)step * K + rank) * TT + warp * S; };
+    auto fetch = [&](int step) {   // one lane
+        const long long t0 = first_row(step);
+        if (step < p.steps && t0 < T) {
+            unsigned char *to = boxes + (size_t)(step % STAGES * kWarps + warp) * kRows;
+            uint64_t *bar = &ex->full[step % STAGES][warp];
+            ptx::mbar_arrive_expect_tx(bar, kRows);
+            ptx::tma_load_3d(ptx::smem_u32(to), &q.gate, cb, (int)t0, b, bar);
+            ptx::tma_load_3d(ptx::smem_u32(to) + S * CH * sizeof(float), &q.x, cb, (int)t0, b, bar);
+        }
+    };
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < STAGES; ++i) fetch(i);
+    }
+    L run = L::all(0.f);
+    if (!PACKED && act && p.state_in) run = L::load(p.state_in + b * C + c0);
+
+    for (int step = 0; step < p.steps; ++step) {
+        const int par = step & 1;
+        const long long t0 = first_row(step);
+        L a[S], u[S];
+        int code[PACKED ? S : 1];
+        if constexpr (PACKED) {
+#pragma unroll
+            for (int s = 0; s < S; ++s) code[s] = 0;
+            if (t0 < T) {
+#pragma unroll
+                for (int s = 0; s < S; s += 4) {
+                    const int4 c = *reinterpret_cast<const int4 *>(p.codes + t0 + s);
+                    code[s] = c.x, code[s + 1] = c.y, code[s + 2] = c.z, code[s + 3] = c.w;
+                }
+            }
+        }
+        if (t0 < T) {
+            ptx::mbar_wait(&ex->full[step % STAGES][warp], (step / STAGES) & 1, &ex->abort, q.err);
+            const unsigned char *at = boxes + (size_t)(step % STAGES * kWarps + warp) * kRows;
+            const float *sa = reinterpret_cast<const float *>(at) + lane * V;
+            const IO *sx = reinterpret_cast<const IO *>(at + S * CH * sizeof(float)) + lane * V;
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                a[s] = L::load(sa + s * CH);
+                u[s] = L::load(sx + s * CH);
+                if (BLEND) u[s] = blended(a[s], u[s]);
+            }
+        }
+        __syncwarp();
+        if (lane == 0) fetch(step + STAGES);   // into the part that the warp has just read
+        if (t0 + S > T) {   // rows behind the end: a = 1, u = 0 leaves the state
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+                if (t0 + s >= T) a[s] = L::all(1.f), u[s] = L::all(0.f);
+        }
+        // the warp's own rows: (P, H).  A sequence's first row starts from its slot of the states;
+        // the row's h replaces its input for the second walk, when the slot may be overwritten.
+        Run<V> own{L::all(1.f), L::all(0.f)};
+        bool reset = false;
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            if constexpr (PACKED) {
+                if (code[s] == 0) continue;
+                if (row_first(code[s])) {
+                    reset = true;
+                    if (act && p.state_in)
+#pragma unroll
+                        for (int j = 0; j < V; ++j)
+                            u[s].set(j, fmaf(a[s].get(j), p.state_in[row_seq(code[s]) * C + c0 + j], u[s].get(j)));
+                    own.H = u[s];
+                    continue;
+                }
+            }
+            own.H = fma(a[s], own.H, u[s]);
+            own.P = mul(own.P, a[s]);
+        }
+        ex->warp[par][warp][lane] = own;
+        if (PACKED && lane == 0) ex->reset[par][warp] = reset;
+        __syncthreads();
+        // the rows of the tile in front of the warp, and the whole tile
+        Run<V> front{L::all(1.f), L::all(0.f)}, all = front;
+        bool front_reset = false, all_reset = false;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w == warp) front = all, front_reset = all_reset;
+            const Run<V> r = ex->warp[par][w][lane];
+            if (PACKED && ex->reset[par][w]) {
+                all = r, all_reset = true;
+            } else {
+                all.H = fma(r.P, all.H, r.H);
+                all.P = mul(all.P, r.P);
+            }
+        }
+        L in = run;
+        if (K > 1) {
+            const uint32_t at = ptx::smem_u32(slots + ((size_t)par * K + rank) * 32 + lane);
+            const uint32_t bar = ptx::smem_u32(&ex->met[par]);
+            for (int to = warp; to < K; to += kWarps) {
+                send(at, bar, to, all);
+                if (PACKED && lane == 0) send(ptx::smem_u32(&ex->slot_reset[par][rank]), bar, to, (int)all_reset);
+            }
+            if (tid == 0) ptx::mbar_arrive_expect_tx(&ex->met[par], K * (32 * (int)sizeof(Run<V>) + (PACKED ? 4 : 0)));
+            ptx::mbar_wait(&ex->met[par], (step >> 1) & 1, &ex->abort, q.err);
+            for (int r = 0; r < K; ++r) {
+                if (r == rank) in = run;
+                const Run<V> e = slots[((size_t)par * K + r) * 32 + lane];
+                run = (PACKED && ex->slot_reset[par][r]) ? e.H : fma(e.P, run, e.H);
+            }
+        } else {
+            run = (PACKED && all_reset) ? all.H : fma(all.P, run, all.H);
+        }
+        L h = (PACKED && front_reset) ? front.H : fma(front.P, in, front.H);
+        if (act && t0 < T) {
+            if (p.ckpt && t0 % kScanCheckpoint == 0) {
+                const long long rows = (T + kScanCheckpoint - 1) / kScanCheckpoint;
+                h.store(p.ckpt + (b * rows + t0 / kScanCheckpoint) * C + c0);
+            }
+            IO *to = hb + t0 * C;
+            auto row = [&](int s) {
+                if constexpr (PACKED) {
+                    if (code[s] == 0) return;
+                    h = row_first(code[s]) ? u[s] : fma(a[s], h, u[s]);
+                    if (row_last(code[s])) {
+#pragma unroll
+                        for (int j = 0; j < V; ++j) p.state_out[row_seq(code[s]) * C + c0 + j] = h.get(j);
+                    }
+                } else {
+                    h = fma(a[s], h, u[s]);
+                }
+                h.store(to + s * C);
+            };
+            if (hb) {
+                if (t0 + S <= T) {
+#pragma unroll
+                    for (int s = 0; s < S; ++s) row(s);
+                } else {
+#pragma unroll
+                    for (int s = 0; s < S; ++s)
+                        if (t0 + s < T) row(s);
+                }
+            }
+        }
+    }
+    if (!PACKED && rank == 0 && warp == 0 && act && p.state_out)
+#pragma unroll
+        for (int j = 0; j < V; ++j) p.state_out[b * C + c0 + j] = run.get(j);
+    if (ex->abort) settle();
+    if (K > 1) {   // no CTA may leave while another one's store to it is in flight
+        cluster_arrive();
+        cluster_wait();
+    }
+}
+
+struct TmaBackwardParams {
+    CUtensorMap gate, x, dh;
+    BackwardParams b;
+    unsigned *err;
+};
+// Shared memory: the ring, [STAGES][kWarps] of (gate, x, dh rows, a checkpoint row); then this.
+template <typename SH, int STAGES>
+struct TmaBackwardExchange {
+    Run<SH::V> warp[2][kWarps][32];   // (P, H) forwards
+    Lane<SH::V> M[2][kWarps][32];
+    uint64_t full[STAGES][kWarps];
+    uint64_t met[2];
+    int abort;
+};
+template <typename IO, typename SH>
+constexpr uint32_t tma_backward_rows_bytes() {
+    return SH::S * SH::CH * (sizeof(float) + 2 * sizeof(IO)) + SH::CH * sizeof(float);
+}
+
+template <typename IO, typename SH, int STAGES, bool BLEND>
+__global__ void __launch_bounds__(kThreads, 2) scan_backward_tma_kernel(const __grid_constant__ TmaBackwardParams q) {
+    constexpr int V = SH::V, S = SH::S, CH = SH::CH, TT = SH::TT;
+    constexpr int kGroups = kScanCheckpoint / S;   // warps between two checkpoints
+    static_assert(kScanCheckpoint % S == 0 && TT % kScanCheckpoint == 0, "tiles hold whole checkpoint spans");
+    constexpr uint32_t kRows = tma_backward_rows_bytes<IO, SH>(), kBoxes = kRows - CH * sizeof(float);
+    using L = Lane<V>;
+    extern __shared__ __align__(128) unsigned char boxes[];
+    auto *ex = reinterpret_cast<TmaBackwardExchange<SH, STAGES> *>(boxes + (size_t)STAGES * kWarps * kRows);
+    auto *slots = reinterpret_cast<Run<V> *>(boxes + (size_t)STAGES * kWarps * kRows +
+                                             (sizeof(TmaBackwardExchange<SH, STAGES>) + 15) / 16 * 16);
+    const BackwardParams &p = q.b;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int K = p.K, rank = blockIdx.x % K;
+    const long long col = blockIdx.x / K;
+    const int b = (int)(col / p.blocks);
+    const int cb = (int)(col % p.blocks) * CH, c0 = cb + lane * V;
+    const bool act = c0 < p.C;
+    const long long T = p.T, C = p.C;
+    const long long tiles = (T + TT - 1) / TT;
+    const float *kb = p.ckpt + (b * ((T + kScanCheckpoint - 1) / kScanCheckpoint)) * C + cb;
+    const uint32_t kept_bytes = (uint32_t)(C - cb < CH ? C - cb : CH) * sizeof(float);
+    IO *ob = static_cast<IO *>(p.dx) + b * T * C + c0;
+    float *gb = p.dgate ? p.dgate + b * T * C + c0 : nullptr;
+    const bool kept = warp % kGroups == 0;   // the warp's rows start at a checkpoint
+
+    if (tid < STAGES * kWarps) ptx::mbar_init(&ex->full[0][0] + tid, 1);
+    if (tid == 0) {
+        ex->abort = 0;
+        ptx::mbar_init(&ex->met[0], 1);
+        ptx::mbar_init(&ex->met[1], 1);
+    }
+    ptx::fence_mbar_init();
+    if (K > 1) {
+        cluster_arrive();
+        cluster_wait();
+    } else {
+        __syncthreads();
+    }
+    auto first_row = [&](int step) { return (tiles - 1 - ((long long)step * K + rank)) * TT + warp * S; };
+    // A warp's rows may lie behind the last row at the first steps, and in front of row 0 at the
+    // last ones: only the loads that were asked for are waited for, and counted for the parity.
+    auto live_at = [&](int step) {
+        const long long t0 = first_row(step);
+        return step < p.steps && t0 >= 0 && t0 < T;
+    };
+    auto fetch = [&](int step) {   // one lane
+        if (live_at(step)) {
+            const long long t0 = first_row(step);
+            const uint32_t to = ptx::smem_u32(boxes + (size_t)(step % STAGES * kWarps + warp) * kRows);
+            uint64_t *bar = &ex->full[step % STAGES][warp];
+            ptx::mbar_arrive_expect_tx(bar, kBoxes + (kept ? kept_bytes : 0));
+            ptx::tma_load_3d(to, &q.gate, cb, (int)t0, b, bar);
+            ptx::tma_load_3d(to + S * CH * sizeof(float), &q.x, cb, (int)t0, b, bar);
+            ptx::tma_load_3d(to + S * CH * (sizeof(float) + sizeof(IO)), &q.dh, cb, (int)t0, b, bar);
+            if (kept) ptx::bulk_load(to + kBoxes, kb + t0 / kScanCheckpoint * C, kept_bytes, bar);
+        }
+    };
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < STAGES; ++i) fetch(i);
+    }
+    uint32_t phases = 0;   // a bit a stage: the parity of its next load
+    L run = L::all(0.f);
+    if (act && p.dstate)
+#pragma unroll
+        for (int j = 0; j < V; ++j) run.set(j, p.dstate[b * C + c0 + j]);
+
+    for (int step = 0; step < p.steps; ++step) {
+        const int par = step & 1, st = step % STAGES;
+        const long long t0 = first_row(step);
+        const bool live = live_at(step);
+        L a[S], x[S], d[S], k = L::all(0.f);
+        if (live) {
+            ptx::mbar_wait(&ex->full[st][warp], (phases >> st) & 1, &ex->abort, q.err);
+            phases ^= 1u << st;
+            const unsigned char *at = boxes + (size_t)(st * kWarps + warp) * kRows;
+            const float *sa = reinterpret_cast<const float *>(at) + lane * V;
+            const IO *sx = reinterpret_cast<const IO *>(at + S * CH * sizeof(float)) + lane * V;
+            const IO *sd = sx + S * CH;
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                a[s] = L::load(sa + s * CH);
+                x[s] = L::load(sx + s * CH);
+                d[s] = L::load(sd + s * CH);
+            }
+            if (kept && act) k = L::load(reinterpret_cast<const float *>(at + kBoxes) + lane * V);
+        }
+        __syncwarp();
+        if (lane == 0) fetch(step + STAGES);
+        if (!live || t0 + S > T) {
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+                if (!live || t0 + s >= T) a[s] = L::all(1.f), x[s] = L::all(0.f), d[s] = L::all(0.f);
+        }
+        // the warp's rows: P, forwards H (from the checkpoint where it has one), backwards M
+        Run<V> own{L::all(1.f), k};
+        L M = L::all(0.f), before[S];
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            own.H = fma(a[s], own.H, BLEND ? blended(a[s], x[s]) : x[s]);
+            own.P = mul(own.P, a[s]);
+        }
+#pragma unroll
+        for (int s = S - 1; s >= 0; --s) M = mul(a[s], add(d[s], M));
+        ex->warp[par][warp][lane] = own;
+        ex->M[par][warp][lane] = M;
+        __syncthreads();
+        // forwards: the state in front of the warp, from the last checkpoint
+        L h = k;
+        if (!kept) {
+            const int from = warp / kGroups * kGroups;
+            h = ex->warp[par][from][lane].H;
+            for (int w = from + 1; w < warp; ++w) {
+                const Run<V> r = ex->warp[par][w][lane];
+                h = fma(r.P, h, r.H);
+            }
+        }
+        // backwards: what the rows of the tile behind the warp do to m, and the whole tile
+        Run<V> behind{L::all(1.f), L::all(0.f)}, all = behind;
+#pragma unroll
+        for (int w = kWarps - 1; w >= 0; --w) {
+            if (w == warp) behind = all;
+            const L P = ex->warp[par][w][lane].P;
+            all.H = fma(P, all.H, ex->M[par][w][lane]);
+            all.P = mul(all.P, P);
+        }
+        L in = run;
+        if (K > 1) {
+            const uint32_t at = ptx::smem_u32(slots + ((size_t)par * K + rank) * 32 + lane);
+            const uint32_t bar = ptx::smem_u32(&ex->met[par]);
+            for (int to = warp; to < K; to += kWarps) send(at, bar, to, all);
+            if (tid == 0) ptx::mbar_arrive_expect_tx(&ex->met[par], K * 32 * (int)sizeof(Run<V>));
+            ptx::mbar_wait(&ex->met[par], (step >> 1) & 1, &ex->abort, q.err);
+            for (int r = 0; r < K; ++r) {
+                if (r == rank) in = run;
+                const Run<V> e = slots[((size_t)par * K + r) * 32 + lane];
+                run = fma(e.P, run, e.H);
+            }
+        } else {
+            run = fma(all.P, run, all.H);
+        }
+        if (act && live) {
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                before[s] = h;
+                h = fma(a[s], h, BLEND ? blended(a[s], x[s]) : x[s]);
+            }
+            L m = fma(behind.P, in, behind.H);
+            const bool full = t0 + S <= T;
+#pragma unroll
+            for (int s = S - 1; s >= 0; --s) {
+                const L l = add(d[s], m);
+                m = mul(a[s], l);
+                if (full || t0 + s < T) {
+                    (BLEND ? blended(a[s], l) : l).store(ob + (t0 + s) * C);
+                    if (gb) {
+                        const L g = BLEND ? add(before[s], mul(x[s], L::all(-1.f))) : before[s];
+                        mul(l, g).store(gb + (t0 + s) * C);
+                    }
+                }
+            }
+        }
+    }
+    if (rank == 0 && warp == 0 && act && p.dstate0)
+#pragma unroll
+        for (int j = 0; j < V; ++j) p.dstate0[b * C + c0 + j] = run.get(j);
+    if (ex->abort) settle();
+    if (K > 1) {   // no CTA may leave while another one's store to it is in flight
+        cluster_arrive();
+        cluster_wait();
+    }
+}
+
 // One token: no reuse, every operand once.  Flat over N * C elements, V a thread (the last ones
 // singly; V = 1 where a tensor starts off the vectors' boundaries).
 template <typename IO, int V, bool BLEND>
@@ -842,6 +1362,88 @@ struct Backward {
     }
 };
 
+// Row tensors as TMA sees them: [B][T][C] in boxes of S rows x CH channels.  False where a row
+// does not start on 16 bytes (or a size is beyond a tensor map).
+template <typename SH>
+bool row_map(CUtensorMap *map, const void *base, size_t elem, long long B, long long T, long long C) {
+    return make_tmap_3d(map, base, elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                        (uint32_t)elem, C, T, B, C * elem, T * C * elem, SH::CH, SH::S, false);
+}
+
+template <typename IO, typename SH, int STAGES, bool BLEND, bool PACKED>
+struct ForwardTma {
+    static constexpr auto kernel = scan_tma_kernel<IO, SH, STAGES, BLEND, PACKED>;
+    static size_t smem(int K) {
+        return (size_t)STAGES * kWarps * tma_rows_bytes<IO, SH>() + (sizeof(TmaExchange<SH, STAGES>) + 15) / 16 * 16 +
+               (K > 1 ? (size_t)2 * K * 32 * sizeof(Run<SH::V>) : 0);
+    }
+    static long long cols(const ScanArgs &a) { return (long long)a.B * ((a.C + SH::CH - 1) / SH::CH); }
+    static long long tiles(const ScanArgs &a) { return ((long long)a.T + SH::TT - 1) / SH::TT; }
+    static Plan plan(const ScanArgs &a) {
+        return plan_clusters<ForwardTma>(cols(a), tiles(a), (double)kThreads * SH::E * (sizeof(float) + 2 * sizeof(IO)));
+    }
+    static cudaError_t launch(const ScanArgs &a, int K) {
+        TmaScanParams q;
+        if (!row_map<SH>(&q.gate, a.gate, sizeof(float), a.B, a.T, a.C) ||
+            !row_map<SH>(&q.x, a.x, sizeof(IO), a.B, a.T, a.C))
+            return cudaErrorInvalidValue;
+        ScanParams &p = q.s;
+        p.x = a.x; p.gate = a.gate;
+        p.state_in = a.state_in; p.state_out = a.state_out;
+        p.h = a.h; p.ckpt = a.ckpt; p.codes = a.codes;
+        p.T = a.T; p.C = a.C;
+        p.blocks = (int)((a.C + SH::CH - 1) / SH::CH);
+        p.K = K;
+        p.steps = (int)((tiles(a) + K - 1) / K);
+        q.err = device_error_word();
+        return launch_cluster<TmaScanParams>(kernel, q, cols(a), K, smem(K), a.stream);
+    }
+};
+
+template <typename IO, typename SH, int STAGES, bool BLEND>
+struct BackwardTma {
+    static constexpr auto kernel = scan_backward_tma_kernel<IO, SH, STAGES, BLEND>;
+    static size_t smem(int K) {
+        return (size_t)STAGES * kWarps * tma_backward_rows_bytes<IO, SH>() +
+               (sizeof(TmaBackwardExchange<SH, STAGES>) + 15) / 16 * 16 +
+               (K > 1 ? (size_t)2 * K * 32 * sizeof(Run<SH::V>) : 0);
+    }
+    static long long cols(const ScanBackwardArgs &a) { return (long long)a.B * ((a.C + SH::CH - 1) / SH::CH); }
+    static long long tiles(const ScanBackwardArgs &a) { return ((long long)a.T + SH::TT - 1) / SH::TT; }
+    static Plan plan(const ScanBackwardArgs &a) {
+        return plan_clusters<BackwardTma>(cols(a), tiles(a),
+                                          (double)kThreads * SH::E * (2 * sizeof(float) + 3 * sizeof(IO)));
+    }
+    static cudaError_t launch(const ScanBackwardArgs &a, int K) {
+        TmaBackwardParams q;
+        if (!row_map<SH>(&q.gate, a.gate, sizeof(float), a.B, a.T, a.C) ||
+            !row_map<SH>(&q.x, a.x, sizeof(IO), a.B, a.T, a.C) || !row_map<SH>(&q.dh, a.dh, sizeof(IO), a.B, a.T, a.C))
+            return cudaErrorInvalidValue;
+        BackwardParams &p = q.b;
+        p.x = a.x; p.dh = a.dh;
+        p.gate = a.gate; p.ckpt = a.ckpt; p.dstate = a.dstate;
+        p.dx = a.dx; p.dgate = a.dgate; p.dstate0 = a.dstate0;
+        p.T = a.T; p.C = a.C;
+        p.blocks = (int)((a.C + SH::CH - 1) / SH::CH);
+        p.K = K;
+        p.steps = (int)((tiles(a) + K - 1) / K);
+        q.err = device_error_word();
+        return launch_cluster<TmaBackwardParams>(kernel, q, cols(a), K, smem(K), a.stream);
+    }
+};
+
+// Whether rows can come by TMA: 16-byte rows and starts (and channels that a lane's vectors and
+// the checkpoints' bulk copies divide), sizes within a tensor map.
+bool tma_rows(long long B, long long T, long long C, size_t elem, std::initializer_list<const void *> in,
+              std::initializer_list<const void *> out) {
+    if (C * elem % 16 || C * 4 % 16 || T * C * 4 >= (1ll << 40)) return false;
+    for (const void *q : in)
+        if (reinterpret_cast<uintptr_t>(q) % 16) return false;
+    for (const void *q : out)
+        if (reinterpret_cast<uintptr_t>(q) % 8) return false;
+    return true;
+}
+
 // Channels a thread: the widest vectors that the rows' length and the tensors' starts allow.
 template <typename IO>
 int vector_width(long long C, std::initializer_list<const void *> io, std::initializer_list<const void *> fp32) {
@@ -872,8 +1474,18 @@ cudaError_t forward_flags(const ScanArgs &a) {
     if (a.codes) return a.blend ? forward_v<IO, V, true, true>(a) : forward_v<IO, V, false, true>(a);
     return a.blend ? forward_v<IO, V, true, false>(a) : forward_v<IO, V, false, false>(a);
 }
+template <typename IO, bool BLEND, bool PACKED>
+cudaError_t forward_tma(const ScanArgs &a) {
+    constexpr int E = sizeof(IO) == 2 ? 32 : 16, STAGES = sizeof(IO) == 2 ? 2 : 3;
+    return launch_best<ForwardTma<IO, TmaShape<2, E>, STAGES, BLEND, PACKED>,
+                       ForwardTma<IO, TmaShape<1, E>, STAGES, BLEND, PACKED>>(a);
+}
 template <typename IO>
 cudaError_t forward_io(const ScanArgs &a) {
+    if (tma_rows(a.B, a.T, a.C, sizeof(IO), {a.x, a.gate}, {a.h, a.ckpt, a.state_in, a.state_out})) {
+        if (a.codes) return a.blend ? forward_tma<IO, true, true>(a) : forward_tma<IO, false, true>(a);
+        return a.blend ? forward_tma<IO, true, false>(a) : forward_tma<IO, false, false>(a);
+    }
     const int V = vector_width<IO>(a.C, {a.x, a.h}, {a.gate, a.ckpt});
     return V == 4 ? forward_flags<IO, 4>(a) : V == 2 ? forward_flags<IO, 2>(a) : forward_flags<IO, 1>(a);
 }
@@ -883,8 +1495,15 @@ cudaError_t backward_v(const ScanBackwardArgs &a) {
     constexpr int E = sizeof(IO) == 2 && V > 1 ? 16 : 8, STAGES = sizeof(IO) == 2 ? 2 : 3;
     return launch_best<Backward<IO, Shape<V, 16, E>, STAGES, BLEND>, Backward<IO, Shape<V, 4, E>, STAGES, BLEND>>(a);
 }
+template <typename IO, bool BLEND>
+cudaError_t backward_tma(const ScanBackwardArgs &a) {
+    constexpr int STAGES = sizeof(IO) == 2 ? 3 : 2;
+    return launch_best<BackwardTma<IO, TmaShape<2, 16>, STAGES, BLEND>, BackwardTma<IO, TmaShape<1, 16>, STAGES, BLEND>>(a);
+}
 template <typename IO>
 cudaError_t backward_io(const ScanBackwardArgs &a) {
+    if (tma_rows(a.B, a.T, a.C, sizeof(IO), {a.x, a.gate, a.dh, a.ckpt}, {a.dx, a.dgate}))
+        return a.blend ? backward_tma<IO, true>(a) : backward_tma<IO, false>(a);
     const int V = vector_width<IO>(a.C, {a.x, a.dh, a.dx}, {a.gate, a.ckpt, a.dgate});
     if (V == 4) return a.blend ? backward_v<IO, 4, true>(a) : backward_v<IO, 4, false>(a);
     if (V == 2) return a.blend ? backward_v<IO, 2, true>(a) : backward_v<IO, 2, false>(a);
