@@ -531,7 +531,7 @@ extern "C" la_status_t la_linear_scan_varlen(la_dtype_t dtype, int N, int T, int
                                              unsigned flags, void *workspace, size_t workspace_bytes, void *stream) {
     timer_reset();
     // a row's sequence number shares a 32-bit code with two flags; the codes are padded rows
-    if (N < 1 || N >= (1 << 29) || T > INT32_MAX - 64) return LA_ERR_INVALID_ARG;
+    if (N < 1 || N >= (1 << 29) || T > INT32_MAX - 512) return LA_ERR_INVALID_ARG;
     if (!scan_sizes_ok(dtype, 1, T, C, flags, LA_FLAG_INIT_STATE | LA_SCAN_BLEND) || (long long)N > kMaxElems / C)
         return LA_ERR_INVALID_ARG;
     if (!tensor_ok(cu_seqlens, 4) || !tensor_ok(state, 4)) return LA_ERR_INVALID_ARG;

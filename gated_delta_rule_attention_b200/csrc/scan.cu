@@ -30,12 +30,9 @@
 // pass needs h_{t-1}: the forward pass keeps the state in front of every 32nd row
 // (`checkpoints`, 1/32 of a fp32 h), from which a tile's rows are walked again on chip, so
 // the backward pass too reads each input once.
-#include "la_internal.cuh"
-#include "ptx.cuh"
-#include "tmap.cuh"
+#include "scan_util.cuh"
 #include "vec.cuh"
 
-#include <atomic>
 #include <initializer_list>
 #include <type_traits>
 
@@ -43,7 +40,6 @@ namespace la {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kMaxCluster = 16;
 
 template <int BYTES>
 __device__ __forceinline__ void copy_async(void *dst, const void *src) {
@@ -55,35 +51,6 @@ template <int N>
 __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-
-// Row codes of a packed batch (one int32 a row, from scan_rows_kernel): 0 for a row of no
-// sequence, else 4 (sequence + 1) + 2 (its last row) + 1 (its first row).
-__device__ __forceinline__ bool row_first(int code) { return code & 1; }
-__device__ __forceinline__ bool row_last(int code) { return code & 2; }
-__device__ __forceinline__ long long row_seq(int code) { return (code >> 2) - 1; }
-
-struct ScanParams {
-    const void *x;
-    const float *gate;
-    const float *state_in;   // [B or N, C]; nullptr: zeros
-    float *state_out;        // [B or N, C]; nullptr: not kept.  May be state_in.
-    void *h;                 // nullptr: not kept
-    float *ckpt;             // [B, ceil(T / 32), C]; nullptr: not kept
-    const int *codes;        // packed: [T rounded up to 32]
-    long long T, C;
-    int blocks;              // channel blocks of one batch row
-    int K;                   // CTAs of a cluster
-    int steps;               // tiles each CTA walks
-};
-
-struct BackwardParams {
-    const void *x, *dh;
-    const float *gate, *ckpt, *dstate;   // dstate: nullptr for zeros
-    void *dx;
-    float *dgate, *dstate0;              // dstate0: nullptr: not kept
-    long long T, C;
-    int blocks, K, steps;
-};
 
 // Shape of a kernel: V channels a thread (one vector load), LC threads side by side, E
 // elements a thread.
@@ -118,13 +85,6 @@ __device__ __forceinline__ void store_cluster(uint32_t addr, uint32_t rank, int 
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(addr), "r"(rank));
     asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(to), "r"(a) : "memory");
 }
-__device__ __forceinline__ void cluster_arrive() {
-    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-}
-
 template <typename IO, typename SH, int STAGES>
 constexpr size_t scan_ring_bytes() {
     return SH::V == 1 ? 0 : (size_t)STAGES * kThreads * SH::E * (sizeof(float) + sizeof(IO));
@@ -657,525 +617,6 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(const Backwa
     }
 }
 
-// ------------------------------------------------------------------------------- rows by TMA
-
-// V neighbouring channels of one lane, as one (V = 1) or packed (V = 2) fp32 operand.
-template <int V>
-struct Lane;
-template <>
-struct Lane<1> {
-    float v;
-    static __device__ __forceinline__ Lane all(float x) { return {x}; }
-    __device__ __forceinline__ float get(int) const { return v; }
-    __device__ __forceinline__ void set(int, float x) { v = x; }
-    static __device__ __forceinline__ Lane load(const float *p) { return {*p}; }
-    static __device__ __forceinline__ Lane load(const __nv_bfloat16 *p) { return {__bfloat162float(*p)}; }
-    __device__ __forceinline__ void store(float *p) const { *p = v; }
-    __device__ __forceinline__ void store(__nv_bfloat16 *p) const { *p = __float2bfloat16_rn(v); }
-};
-template <>
-struct Lane<2> {
-    unsigned long long v;
-    static __device__ __forceinline__ Lane make(float a, float b) {
-        Lane r;
-        asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-        return r;
-    }
-    static __device__ __forceinline__ Lane all(float x) { return make(x, x); }
-    __device__ __forceinline__ float2 both() const {
-        float2 r;
-        asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-        return r;
-    }
-    __device__ __forceinline__ float get(int j) const { return j ? both().y : both().x; }
-    __device__ __forceinline__ void set(int j, float x) {
-        const float2 b = both();
-        *this = j ? make(b.x, x) : make(x, b.y);
-    }
-    static __device__ __forceinline__ Lane load(const float *p) {
-        const float2 f = *reinterpret_cast<const float2 *>(p);
-        return make(f.x, f.y);
-    }
-    static __device__ __forceinline__ Lane load(const __nv_bfloat16 *p) {
-        const uint32_t w = *reinterpret_cast<const uint32_t *>(p);   // bf16 -> fp32: the high half
-        return make(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-    }
-    __device__ __forceinline__ void store(float *p) const { *reinterpret_cast<float2 *>(p) = both(); }
-    __device__ __forceinline__ void store(__nv_bfloat16 *p) const {
-        const float2 f = both();
-        *reinterpret_cast<uint32_t *>(p) = ptx::pack_bf16x2(f.x, f.y);
-    }
-};
-__device__ __forceinline__ Lane<1> fma(Lane<1> a, Lane<1> b, Lane<1> c) { return {fmaf(a.v, b.v, c.v)}; }
-__device__ __forceinline__ Lane<1> mul(Lane<1> a, Lane<1> b) { return {a.v * b.v}; }
-__device__ __forceinline__ Lane<1> add(Lane<1> a, Lane<1> b) { return {a.v + b.v}; }
-__device__ __forceinline__ Lane<2> fma(Lane<2> a, Lane<2> b, Lane<2> c) {
-    Lane<2> r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
-__device__ __forceinline__ Lane<2> mul(Lane<2> a, Lane<2> b) {
-    Lane<2> r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ Lane<2> add(Lane<2> a, Lane<2> b) {
-    Lane<2> r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-// (1 - a) x with one rounding of the exact x - a x
-template <int V>
-__device__ __forceinline__ Lane<V> blended(Lane<V> a, Lane<V> x) {
-    return fma(mul(a, Lane<V>::all(-1.f)), x, x);
-}
-
-// (P, H) of a run of rows, one lane's channels.
-template <int V>
-struct alignas(8 * V) Run {
-    Lane<V> P, H;
-};
-// To shared memory of CTA `rank` of the cluster; the bytes count towards its barrier `bar` (both
-// given by this CTA's own addresses).
-__device__ __forceinline__ uint32_t of_rank(uint32_t addr, uint32_t rank) {
-    uint32_t to;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(addr), "r"(rank));
-    return to;
-}
-__device__ __forceinline__ void send(uint32_t addr, uint32_t bar, uint32_t rank, const Run<1> &r) {
-    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(
-                     of_rank(addr, rank)),
-                 "f"(r.P.v), "f"(r.H.v), "r"(of_rank(bar, rank))
-                 : "memory");
-}
-__device__ __forceinline__ void send(uint32_t addr, uint32_t bar, uint32_t rank, const Run<2> &r) {
-    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b64 [%0], {%1, %2}, [%3];" ::"r"(
-                     of_rank(addr, rank)),
-                 "l"(r.P.v), "l"(r.H.v), "r"(of_rank(bar, rank))
-                 : "memory");
-}
-__device__ __forceinline__ void send(uint32_t addr, uint32_t bar, uint32_t rank, int v) {
-    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.s32 [%0], %1, [%2];" ::"r"(of_rank(addr, rank)),
-                 "r"(v), "r"(of_rank(bar, rank))
-                 : "memory");
-}
-
-struct TmaScanParams {
-    CUtensorMap gate, x;     // [B][T][C], boxes of S rows x 32 V channels
-    ScanParams s;
-    unsigned *err;
-};
-
-// After a wait that ran out: give the copies still in flight 10 ms to land before the block's
-// shared memory goes.
-__device__ __noinline__ void settle() {
-    for (int i = 0; i < 1000; ++i) __nanosleep(10000);
-}
-
-// Shape: V channels a lane, E elements a thread; a warp has S rows of 32 V channels.
-template <int V_, int E_>
-struct TmaShape {
-    static constexpr int V = V_, E = E_, S = E / V, CH = 32 * V, TT = kWarps * S;
-};
-
-// Shared memory: the ring, [STAGES][kWarps] of (gate rows, x rows); then this.
-template <typename SH, int STAGES>
-struct TmaExchange {
-    Run<SH::V> warp[2][kWarps][32];   // by the step's parity
-    uint64_t full[STAGES][kWarps];
-    uint64_t met[2];                  // K > 1: the step's runs of all ranks are here
-    int reset[2][kWarps];
-    int slot_reset[2][kMaxCluster];
-    int abort;
-    // followed, on 16 bytes, by Run slot[2][K][32]
-};
-template <typename IO, typename SH>
-constexpr uint32_t tma_rows_bytes() { return SH::S * SH::CH * (sizeof(float) + sizeof(IO)); }
-
-// Each warp runs its own pipeline: one lane asks for the boxes of the warp's rows, STAGES steps
-// ahead, into a part of the ring that only this warp reads.  All lanes of a warp hold the same
-// rows, so rows behind the end, sequence starts and full tiles are decided for the whole warp.
-// Every thread folds the eight warps' (P, H) of its channels itself, and with K > 1 the K
-// CTAs', so a step has one barrier of the CTA and no thread waits for another's fold.  With K > 1
-// the ranks' runs are sent to each other by st.async, whose bytes complete the receiver's
-// barrier of the step's parity.  A slot is written again two steps later: its sender has then
-// had this CTA's run of the step between, sent after all of this CTA had read the slot.
-template <typename IO, typename SH, int STAGES, bool BLEND, bool PACKED>
-__global__ void __launch_bounds__(kThreads, 2) scan_tma_kernel(const __grid_constant__ TmaScanParams q) {
-    constexpr int V = SH::V, S = SH::S, CH = SH::CH, TT = SH::TT;
-    constexpr uint32_t kRows = tma_rows_bytes<IO, SH>();
-    using L = Lane<V>;
-    extern __shared__ __align__(128) unsigned char boxes[];
-    auto *ex = reinterpret_cast<TmaExchange<SH, STAGES> *>(boxes + (size_t)STAGES * kWarps * kRows);
-    auto *slots = reinterpret_cast<Run<V> *>(boxes + (size_t)STAGES * kWarps * kRows +
-                                             (sizeof(TmaExchange<SH, STAGES>) + 15) / 16 * 16);
-    const ScanParams &p = q.s;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int K = p.K, rank = blockIdx.x % K;
-    const long long col = blockIdx.x / K;
-    const int b = (int)(col / p.blocks);
-    const int cb = (int)(col % p.blocks) * CH, c0 = cb + lane * V;
-    const bool act = c0 < p.C;
-    const long long T = p.T, C = p.C;
-    IO *hb = p.h ? static_cast<IO *>(p.h) + b * T * C + c0 : nullptr;
-
-    if (tid < STAGES * kWarps) ptx::mbar_init(&ex->full[0][0] + tid, 1);
-    if (tid == 0) {
-        ex->abort = 0;
-        ptx::mbar_init(&ex->met[0], 1);
-        ptx::mbar_init(&ex->met[1], 1);
-    }
-    ptx::fence_mbar_init();
-    if (K > 1) {   // also: every CTA of the cluster runs before the first store to its shared memory
-        cluster_arrive();
-        cluster_wait();
-    } else {
-        __syncthreads();
-    }
-    auto first_row = [&](int step) { return ((long long)step * K + rank) * TT + warp * S; };
-    auto fetch = [&](int step) {   // one lane
-        const long long t0 = first_row(step);
-        if (step < p.steps && t0 < T) {
-            unsigned char *to = boxes + (size_t)(step % STAGES * kWarps + warp) * kRows;
-            uint64_t *bar = &ex->full[step % STAGES][warp];
-            ptx::mbar_arrive_expect_tx(bar, kRows);
-            ptx::tma_load_3d(ptx::smem_u32(to), &q.gate, cb, (int)t0, b, bar);
-            ptx::tma_load_3d(ptx::smem_u32(to) + S * CH * sizeof(float), &q.x, cb, (int)t0, b, bar);
-        }
-    };
-    if (lane == 0) {
-#pragma unroll
-        for (int i = 0; i < STAGES; ++i) fetch(i);
-    }
-    L run = L::all(0.f);
-    if (!PACKED && act && p.state_in) run = L::load(p.state_in + b * C + c0);
-
-    for (int step = 0; step < p.steps; ++step) {
-        const int par = step & 1;
-        const long long t0 = first_row(step);
-        L a[S], u[S];
-        int code[PACKED ? S : 1];
-        if constexpr (PACKED) {
-#pragma unroll
-            for (int s = 0; s < S; ++s) code[s] = 0;
-            if (t0 < T) {
-#pragma unroll
-                for (int s = 0; s < S; s += 4) {
-                    const int4 c = *reinterpret_cast<const int4 *>(p.codes + t0 + s);
-                    code[s] = c.x, code[s + 1] = c.y, code[s + 2] = c.z, code[s + 3] = c.w;
-                }
-            }
-        }
-        if (t0 < T) {
-            ptx::mbar_wait(&ex->full[step % STAGES][warp], (step / STAGES) & 1, &ex->abort, q.err);
-            const unsigned char *at = boxes + (size_t)(step % STAGES * kWarps + warp) * kRows;
-            const float *sa = reinterpret_cast<const float *>(at) + lane * V;
-            const IO *sx = reinterpret_cast<const IO *>(at + S * CH * sizeof(float)) + lane * V;
-#pragma unroll
-            for (int s = 0; s < S; ++s) {
-                a[s] = L::load(sa + s * CH);
-                u[s] = L::load(sx + s * CH);
-                if (BLEND) u[s] = blended(a[s], u[s]);
-            }
-        }
-        __syncwarp();
-        if (lane == 0) fetch(step + STAGES);   // into the part that the warp has just read
-        if (t0 + S > T) {   // rows behind the end: a = 1, u = 0 leaves the state
-#pragma unroll
-            for (int s = 0; s < S; ++s)
-                if (t0 + s >= T) a[s] = L::all(1.f), u[s] = L::all(0.f);
-        }
-        // the warp's own rows: (P, H).  A sequence's first row starts from its slot of the states;
-        // the row's h replaces its input for the second walk, when the slot may be overwritten.
-        Run<V> own{L::all(1.f), L::all(0.f)};
-        bool reset = false;
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-            if constexpr (PACKED) {
-                if (code[s] == 0) continue;
-                if (row_first(code[s])) {
-                    reset = true;
-                    if (act && p.state_in)
-#pragma unroll
-                        for (int j = 0; j < V; ++j)
-                            u[s].set(j, fmaf(a[s].get(j), p.state_in[row_seq(code[s]) * C + c0 + j], u[s].get(j)));
-                    own.H = u[s];
-                    continue;
-                }
-            }
-            own.H = fma(a[s], own.H, u[s]);
-            own.P = mul(own.P, a[s]);
-        }
-        ex->warp[par][warp][lane] = own;
-        if (PACKED && lane == 0) ex->reset[par][warp] = reset;
-        __syncthreads();
-        // the rows of the tile in front of the warp, and the whole tile
-        Run<V> front{L::all(1.f), L::all(0.f)}, all = front;
-        bool front_reset = false, all_reset = false;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            if (w == warp) front = all, front_reset = all_reset;
-            const Run<V> r = ex->warp[par][w][lane];
-            if (PACKED && ex->reset[par][w]) {
-                all = r, all_reset = true;
-            } else {
-                all.H = fma(r.P, all.H, r.H);
-                all.P = mul(all.P, r.P);
-            }
-        }
-        L in = run;
-        if (K > 1) {
-            const uint32_t at = ptx::smem_u32(slots + ((size_t)par * K + rank) * 32 + lane);
-            const uint32_t bar = ptx::smem_u32(&ex->met[par]);
-            for (int to = warp; to < K; to += kWarps) {
-                send(at, bar, to, all);
-                if (PACKED && lane == 0) send(ptx::smem_u32(&ex->slot_reset[par][rank]), bar, to, (int)all_reset);
-            }
-            if (tid == 0) ptx::mbar_arrive_expect_tx(&ex->met[par], K * (32 * (int)sizeof(Run<V>) + (PACKED ? 4 : 0)));
-            ptx::mbar_wait(&ex->met[par], (step >> 1) & 1, &ex->abort, q.err);
-            for (int r = 0; r < K; ++r) {
-                if (r == rank) in = run;
-                const Run<V> e = slots[((size_t)par * K + r) * 32 + lane];
-                run = (PACKED && ex->slot_reset[par][r]) ? e.H : fma(e.P, run, e.H);
-            }
-        } else {
-            run = (PACKED && all_reset) ? all.H : fma(all.P, run, all.H);
-        }
-        L h = (PACKED && front_reset) ? front.H : fma(front.P, in, front.H);
-        if (act && t0 < T) {
-            if (p.ckpt && t0 % kScanCheckpoint == 0) {
-                const long long rows = (T + kScanCheckpoint - 1) / kScanCheckpoint;
-                h.store(p.ckpt + (b * rows + t0 / kScanCheckpoint) * C + c0);
-            }
-            IO *to = hb + t0 * C;
-            auto row = [&](int s) {
-                if constexpr (PACKED) {
-                    if (code[s] == 0) return;
-                    h = row_first(code[s]) ? u[s] : fma(a[s], h, u[s]);
-                    if (row_last(code[s])) {
-#pragma unroll
-                        for (int j = 0; j < V; ++j) p.state_out[row_seq(code[s]) * C + c0 + j] = h.get(j);
-                    }
-                } else {
-                    h = fma(a[s], h, u[s]);
-                }
-                h.store(to + s * C);
-            };
-            if (hb) {
-                if (t0 + S <= T) {
-#pragma unroll
-                    for (int s = 0; s < S; ++s) row(s);
-                } else {
-#pragma unroll
-                    for (int s = 0; s < S; ++s)
-                        if (t0 + s < T) row(s);
-                }
-            }
-        }
-    }
-    if (!PACKED && rank == 0 && warp == 0 && act && p.state_out)
-#pragma unroll
-        for (int j = 0; j < V; ++j) p.state_out[b * C + c0 + j] = run.get(j);
-    if (ex->abort) settle();
-    if (K > 1) {   // no CTA may leave while another one's store to it is in flight
-        cluster_arrive();
-        cluster_wait();
-    }
-}
-
-struct TmaBackwardParams {
-    CUtensorMap gate, x, dh;
-    BackwardParams b;
-    unsigned *err;
-};
-// Shared memory: the ring, [STAGES][kWarps] of (gate, x, dh rows, a checkpoint row); then this.
-template <typename SH, int STAGES>
-struct TmaBackwardExchange {
-    Run<SH::V> warp[2][kWarps][32];   // (P, H) forwards
-    Lane<SH::V> M[2][kWarps][32];
-    uint64_t full[STAGES][kWarps];
-    uint64_t met[2];
-    int abort;
-};
-template <typename IO, typename SH>
-constexpr uint32_t tma_backward_rows_bytes() {
-    return SH::S * SH::CH * (sizeof(float) + 2 * sizeof(IO)) + SH::CH * sizeof(float);
-}
-
-template <typename IO, typename SH, int STAGES, bool BLEND>
-__global__ void __launch_bounds__(kThreads, 2) scan_backward_tma_kernel(const __grid_constant__ TmaBackwardParams q) {
-    constexpr int V = SH::V, S = SH::S, CH = SH::CH, TT = SH::TT;
-    constexpr int kGroups = kScanCheckpoint / S;   // warps between two checkpoints
-    static_assert(kScanCheckpoint % S == 0 && TT % kScanCheckpoint == 0, "tiles hold whole checkpoint spans");
-    constexpr uint32_t kRows = tma_backward_rows_bytes<IO, SH>(), kBoxes = kRows - CH * sizeof(float);
-    using L = Lane<V>;
-    extern __shared__ __align__(128) unsigned char boxes[];
-    auto *ex = reinterpret_cast<TmaBackwardExchange<SH, STAGES> *>(boxes + (size_t)STAGES * kWarps * kRows);
-    auto *slots = reinterpret_cast<Run<V> *>(boxes + (size_t)STAGES * kWarps * kRows +
-                                             (sizeof(TmaBackwardExchange<SH, STAGES>) + 15) / 16 * 16);
-    const BackwardParams &p = q.b;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int K = p.K, rank = blockIdx.x % K;
-    const long long col = blockIdx.x / K;
-    const int b = (int)(col / p.blocks);
-    const int cb = (int)(col % p.blocks) * CH, c0 = cb + lane * V;
-    const bool act = c0 < p.C;
-    const long long T = p.T, C = p.C;
-    const long long tiles = (T + TT - 1) / TT;
-    const float *kb = p.ckpt + (b * ((T + kScanCheckpoint - 1) / kScanCheckpoint)) * C + cb;
-    const uint32_t kept_bytes = (uint32_t)(C - cb < CH ? C - cb : CH) * sizeof(float);
-    IO *ob = static_cast<IO *>(p.dx) + b * T * C + c0;
-    float *gb = p.dgate ? p.dgate + b * T * C + c0 : nullptr;
-    const bool kept = warp % kGroups == 0;   // the warp's rows start at a checkpoint
-
-    if (tid < STAGES * kWarps) ptx::mbar_init(&ex->full[0][0] + tid, 1);
-    if (tid == 0) {
-        ex->abort = 0;
-        ptx::mbar_init(&ex->met[0], 1);
-        ptx::mbar_init(&ex->met[1], 1);
-    }
-    ptx::fence_mbar_init();
-    if (K > 1) {
-        cluster_arrive();
-        cluster_wait();
-    } else {
-        __syncthreads();
-    }
-    auto first_row = [&](int step) { return (tiles - 1 - ((long long)step * K + rank)) * TT + warp * S; };
-    // A warp's rows may lie behind the last row at the first steps, and in front of row 0 at the
-    // last ones: only the loads that were asked for are waited for, and counted for the parity.
-    auto live_at = [&](int step) {
-        const long long t0 = first_row(step);
-        return step < p.steps && t0 >= 0 && t0 < T;
-    };
-    auto fetch = [&](int step) {   // one lane
-        if (live_at(step)) {
-            const long long t0 = first_row(step);
-            const uint32_t to = ptx::smem_u32(boxes + (size_t)(step % STAGES * kWarps + warp) * kRows);
-            uint64_t *bar = &ex->full[step % STAGES][warp];
-            ptx::mbar_arrive_expect_tx(bar, kBoxes + (kept ? kept_bytes : 0));
-            ptx::tma_load_3d(to, &q.gate, cb, (int)t0, b, bar);
-            ptx::tma_load_3d(to + S * CH * sizeof(float), &q.x, cb, (int)t0, b, bar);
-            ptx::tma_load_3d(to + S * CH * (sizeof(float) + sizeof(IO)), &q.dh, cb, (int)t0, b, bar);
-            if (kept) ptx::bulk_load(to + kBoxes, kb + t0 / kScanCheckpoint * C, kept_bytes, bar);
-        }
-    };
-    if (lane == 0) {
-#pragma unroll
-        for (int i = 0; i < STAGES; ++i) fetch(i);
-    }
-    uint32_t phases = 0;   // a bit a stage: the parity of its next load
-    L run = L::all(0.f);
-    if (act && p.dstate)
-#pragma unroll
-        for (int j = 0; j < V; ++j) run.set(j, p.dstate[b * C + c0 + j]);
-
-    for (int step = 0; step < p.steps; ++step) {
-        const int par = step & 1, st = step % STAGES;
-        const long long t0 = first_row(step);
-        const bool live = live_at(step);
-        L a[S], x[S], d[S], k = L::all(0.f);
-        if (live) {
-            ptx::mbar_wait(&ex->full[st][warp], (phases >> st) & 1, &ex->abort, q.err);
-            phases ^= 1u << st;
-            const unsigned char *at = boxes + (size_t)(st * kWarps + warp) * kRows;
-            const float *sa = reinterpret_cast<const float *>(at) + lane * V;
-            const IO *sx = reinterpret_cast<const IO *>(at + S * CH * sizeof(float)) + lane * V;
-            const IO *sd = sx + S * CH;
-#pragma unroll
-            for (int s = 0; s < S; ++s) {
-                a[s] = L::load(sa + s * CH);
-                x[s] = L::load(sx + s * CH);
-                d[s] = L::load(sd + s * CH);
-            }
-            if (kept && act) k = L::load(reinterpret_cast<const float *>(at + kBoxes) + lane * V);
-        }
-        __syncwarp();
-        if (lane == 0) fetch(step + STAGES);
-        if (!live || t0 + S > T) {
-#pragma unroll
-            for (int s = 0; s < S; ++s)
-                if (!live || t0 + s >= T) a[s] = L::all(1.f), x[s] = L::all(0.f), d[s] = L::all(0.f);
-        }
-        // the warp's rows: P, forwards H (from the checkpoint where it has one), backwards M
-        Run<V> own{L::all(1.f), k};
-        L M = L::all(0.f), before[S];
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-            own.H = fma(a[s], own.H, BLEND ? blended(a[s], x[s]) : x[s]);
-            own.P = mul(own.P, a[s]);
-        }
-#pragma unroll
-        for (int s = S - 1; s >= 0; --s) M = mul(a[s], add(d[s], M));
-        ex->warp[par][warp][lane] = own;
-        ex->M[par][warp][lane] = M;
-        __syncthreads();
-        // forwards: the state in front of the warp, from the last checkpoint
-        L h = k;
-        if (!kept) {
-            const int from = warp / kGroups * kGroups;
-            h = ex->warp[par][from][lane].H;
-            for (int w = from + 1; w < warp; ++w) {
-                const Run<V> r = ex->warp[par][w][lane];
-                h = fma(r.P, h, r.H);
-            }
-        }
-        // backwards: what the rows of the tile behind the warp do to m, and the whole tile
-        Run<V> behind{L::all(1.f), L::all(0.f)}, all = behind;
-#pragma unroll
-        for (int w = kWarps - 1; w >= 0; --w) {
-            if (w == warp) behind = all;
-            const L P = ex->warp[par][w][lane].P;
-            all.H = fma(P, all.H, ex->M[par][w][lane]);
-            all.P = mul(all.P, P);
-        }
-        L in = run;
-        if (K > 1) {
-            const uint32_t at = ptx::smem_u32(slots + ((size_t)par * K + rank) * 32 + lane);
-            const uint32_t bar = ptx::smem_u32(&ex->met[par]);
-            for (int to = warp; to < K; to += kWarps) send(at, bar, to, all);
-            if (tid == 0) ptx::mbar_arrive_expect_tx(&ex->met[par], K * 32 * (int)sizeof(Run<V>));
-            ptx::mbar_wait(&ex->met[par], (step >> 1) & 1, &ex->abort, q.err);
-            for (int r = 0; r < K; ++r) {
-                if (r == rank) in = run;
-                const Run<V> e = slots[((size_t)par * K + r) * 32 + lane];
-                run = fma(e.P, run, e.H);
-            }
-        } else {
-            run = fma(all.P, run, all.H);
-        }
-        if (act && live) {
-#pragma unroll
-            for (int s = 0; s < S; ++s) {
-                before[s] = h;
-                h = fma(a[s], h, BLEND ? blended(a[s], x[s]) : x[s]);
-            }
-            L m = fma(behind.P, in, behind.H);
-            const bool full = t0 + S <= T;
-#pragma unroll
-            for (int s = S - 1; s >= 0; --s) {
-                const L l = add(d[s], m);
-                m = mul(a[s], l);
-                if (full || t0 + s < T) {
-                    (BLEND ? blended(a[s], l) : l).store(ob + (t0 + s) * C);
-                    if (gb) {
-                        const L g = BLEND ? add(before[s], mul(x[s], L::all(-1.f))) : before[s];
-                        mul(l, g).store(gb + (t0 + s) * C);
-                    }
-                }
-            }
-        }
-    }
-    if (rank == 0 && warp == 0 && act && p.dstate0)
-#pragma unroll
-        for (int j = 0; j < V; ++j) p.dstate0[b * C + c0 + j] = run.get(j);
-    if (ex->abort) settle();
-    if (K > 1) {   // no CTA may leave while another one's store to it is in flight
-        cluster_arrive();
-        cluster_wait();
-    }
-}
-
 // One token: no reuse, every operand once.  Flat over N * C elements, V a thread (the last ones
 // singly; V = 1 where a tensor starts off the vectors' boundaries).
 template <typename IO, int V, bool BLEND>
@@ -1237,212 +678,35 @@ scan_rows_kernel(int T, int padded, int row_blocks, int N, long long C, const in
 
 // ------------------------------------------------------------------------------- host side
 
-// How the columns (batch rows x channel blocks) and the tiles of a call are spread: the
-// cluster width whose estimated time is the least.  A CTA alone moves at most `kCtaRate`
-// bytes/ns (its ring's bytes over the latency of HBM under load) and all of them together
-// `kRate`; clusters that do not fit at once take further waves.
-constexpr double kCtaRate = 40.0, kRate = 6500.0;
-
-struct Plan {
-    int K = 1;
-    double cost = 1e300;
-};
-
-template <typename L>   // L: Forward or Backward, one kernel
-Plan plan_clusters(long long cols, long long tiles, double tile_bytes) {
-    // clusters of 2^i CTAs that run at once, plus one (0: not asked yet); the same on every B200
-    static std::atomic<int> known[5];
-    constexpr auto kernel = L::kernel;
-    Plan best;
-    for (int i = 0; i < 5; ++i) {
-        const int K = 1 << i;
-        if (K > 1 && K >= 2 * tiles) break;
-        int fit = known[i].load(std::memory_order_relaxed) - 1;
-        if (fit < 0) {
-            const size_t smem = L::smem(K);
-            if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
-                (K > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)) {
-                (void)cudaGetLastError();
-                break;
-            }
-            cudaLaunchConfig_t cfg = {};
-            cudaLaunchAttribute at[1];
-            at[0].id = cudaLaunchAttributeClusterDimension;
-            at[0].val.clusterDim = {(unsigned)K, 1, 1};
-            cfg.gridDim = dim3(K * 1024);
-            cfg.blockDim = dim3(kThreads);
-            cfg.dynamicSmemBytes = smem;
-            cfg.attrs = at;
-            cfg.numAttrs = 1;
-            int n = 0;
-            if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
-                (void)cudaGetLastError();
-                n = 0;
-            }
-            fit = n;
-            known[i].store(n + 1, std::memory_order_relaxed);
-        }
-        if (fit < 1) continue;
-        const double waves = (double)((cols + fit - 1) / fit);
-        const double active = (double)(cols < fit ? cols : fit) * K;
-        const double steps = (double)((tiles + K - 1) / K);
-        const double rate = active * kCtaRate < kRate ? kCtaRate : kRate / active;
-        const double cost = waves * steps * (tile_bytes / rate + (K > 1 ? 300.0 : 0.0));
-        if (cost < best.cost) best.cost = cost, best.K = K;
-    }
-    return best;
-}
-
-template <typename P>
-cudaError_t launch_cluster(void (*kernel)(P), const P &p, long long cols, int K, size_t smem, cudaStream_t stream) {
-    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (err == cudaSuccess && K > 8)
-        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (err != cudaSuccess) return err;
-    if (cols * K > INT32_MAX) return cudaErrorInvalidConfiguration;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim = {(unsigned)K, 1, 1};
-    cfg.gridDim = dim3((unsigned)(cols * K));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    timer_begin(stream);
-    err = cudaLaunchKernelEx(&cfg, kernel, p);
-    timer_end(stream);
-    note_launches(1);
-    return err != cudaSuccess ? err : cudaGetLastError();
-}
-
 template <typename IO, typename SH, int STAGES, bool BLEND, bool PACKED>
 struct Forward {
     static constexpr auto kernel = scan_kernel<IO, SH, STAGES, BLEND, PACKED>;
+    static constexpr int kBlock = kThreads, kChannels = SH::CH, kMost = 16;
+    static constexpr double kRate = 4000.0;
+    static constexpr double kTileBytes = (double)kThreads * SH::E * (sizeof(float) + 2 * sizeof(IO));
+    static double step_ns(int K) { return 2200.0 + (K > 1 ? 300.0 : 0.0); }
     static size_t smem(int K) { return scan_ring_bytes<IO, SH, STAGES>() + exchange_bytes<SH>(K); }
     static long long cols(const ScanArgs &a) { return (long long)a.B * ((a.C + SH::CH - 1) / SH::CH); }
     static long long tiles(const ScanArgs &a) { return ((long long)a.T + SH::TT - 1) / SH::TT; }
-    static Plan plan(const ScanArgs &a) {
-        return plan_clusters<Forward>(cols(a), tiles(a), (double)kThreads * SH::E * (sizeof(float) + 2 * sizeof(IO)));
-    }
     static cudaError_t launch(const ScanArgs &a, int K) {
-        ScanParams p;
-        p.x = a.x; p.gate = a.gate;
-        p.state_in = a.state_in; p.state_out = a.state_out;
-        p.h = a.h; p.ckpt = a.ckpt; p.codes = a.codes;
-        p.T = a.T; p.C = a.C;
-        p.blocks = (int)((a.C + SH::CH - 1) / SH::CH);
-        p.K = K;
-        p.steps = (int)((tiles(a) + K - 1) / K);
-        return launch_cluster<ScanParams>(kernel, p, cols(a), K, smem(K), a.stream);
+        return launch_cluster<Forward>(scan_params<Forward>(a, K), cols(a), K, a.stream);
     }
 };
 
 template <typename IO, typename SH, int STAGES, bool BLEND>
 struct Backward {
     static constexpr auto kernel = scan_backward_kernel<IO, SH, STAGES, BLEND>;
+    static constexpr int kBlock = kThreads, kChannels = SH::CH, kMost = 16;
+    static constexpr double kRate = 4000.0;
+    static constexpr double kTileBytes = (double)kThreads * SH::E * (2 * sizeof(float) + 3 * sizeof(IO));
+    static double step_ns(int K) { return 2200.0 + (K > 1 ? 300.0 : 0.0); }
     static size_t smem(int K) { return backward_ring_bytes<IO, SH, STAGES>() + exchange_bytes<SH>(K); }
     static long long cols(const ScanBackwardArgs &a) { return (long long)a.B * ((a.C + SH::CH - 1) / SH::CH); }
     static long long tiles(const ScanBackwardArgs &a) { return ((long long)a.T + SH::TT - 1) / SH::TT; }
-    static Plan plan(const ScanBackwardArgs &a) {
-        return plan_clusters<Backward>(cols(a), tiles(a),
-                                       (double)kThreads * SH::E * (2 * sizeof(float) + 3 * sizeof(IO)));
-    }
     static cudaError_t launch(const ScanBackwardArgs &a, int K) {
-        BackwardParams p;
-        p.x = a.x; p.dh = a.dh;
-        p.gate = a.gate; p.ckpt = a.ckpt; p.dstate = a.dstate;
-        p.dx = a.dx; p.dgate = a.dgate; p.dstate0 = a.dstate0;
-        p.T = a.T; p.C = a.C;
-        p.blocks = (int)((a.C + SH::CH - 1) / SH::CH);
-        p.K = K;
-        p.steps = (int)((tiles(a) + K - 1) / K);
-        return launch_cluster<BackwardParams>(kernel, p, cols(a), K, smem(K), a.stream);
+        return launch_cluster<Backward>(backward_params<Backward>(a, K), cols(a), K, a.stream);
     }
 };
-
-// Row tensors as TMA sees them: [B][T][C] in boxes of S rows x CH channels.  False where a row
-// does not start on 16 bytes (or a size is beyond a tensor map).
-template <typename SH>
-bool row_map(CUtensorMap *map, const void *base, size_t elem, long long B, long long T, long long C) {
-    return make_tmap_3d(map, base, elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
-                        (uint32_t)elem, C, T, B, C * elem, T * C * elem, SH::CH, SH::S, false);
-}
-
-template <typename IO, typename SH, int STAGES, bool BLEND, bool PACKED>
-struct ForwardTma {
-    static constexpr auto kernel = scan_tma_kernel<IO, SH, STAGES, BLEND, PACKED>;
-    static size_t smem(int K) {
-        return (size_t)STAGES * kWarps * tma_rows_bytes<IO, SH>() + (sizeof(TmaExchange<SH, STAGES>) + 15) / 16 * 16 +
-               (K > 1 ? (size_t)2 * K * 32 * sizeof(Run<SH::V>) : 0);
-    }
-    static long long cols(const ScanArgs &a) { return (long long)a.B * ((a.C + SH::CH - 1) / SH::CH); }
-    static long long tiles(const ScanArgs &a) { return ((long long)a.T + SH::TT - 1) / SH::TT; }
-    static Plan plan(const ScanArgs &a) {
-        return plan_clusters<ForwardTma>(cols(a), tiles(a), (double)kThreads * SH::E * (sizeof(float) + 2 * sizeof(IO)));
-    }
-    static cudaError_t launch(const ScanArgs &a, int K) {
-        TmaScanParams q;
-        if (!row_map<SH>(&q.gate, a.gate, sizeof(float), a.B, a.T, a.C) ||
-            !row_map<SH>(&q.x, a.x, sizeof(IO), a.B, a.T, a.C))
-            return cudaErrorInvalidValue;
-        ScanParams &p = q.s;
-        p.x = a.x; p.gate = a.gate;
-        p.state_in = a.state_in; p.state_out = a.state_out;
-        p.h = a.h; p.ckpt = a.ckpt; p.codes = a.codes;
-        p.T = a.T; p.C = a.C;
-        p.blocks = (int)((a.C + SH::CH - 1) / SH::CH);
-        p.K = K;
-        p.steps = (int)((tiles(a) + K - 1) / K);
-        q.err = device_error_word();
-        return launch_cluster<TmaScanParams>(kernel, q, cols(a), K, smem(K), a.stream);
-    }
-};
-
-template <typename IO, typename SH, int STAGES, bool BLEND>
-struct BackwardTma {
-    static constexpr auto kernel = scan_backward_tma_kernel<IO, SH, STAGES, BLEND>;
-    static size_t smem(int K) {
-        return (size_t)STAGES * kWarps * tma_backward_rows_bytes<IO, SH>() +
-               (sizeof(TmaBackwardExchange<SH, STAGES>) + 15) / 16 * 16 +
-               (K > 1 ? (size_t)2 * K * 32 * sizeof(Run<SH::V>) : 0);
-    }
-    static long long cols(const ScanBackwardArgs &a) { return (long long)a.B * ((a.C + SH::CH - 1) / SH::CH); }
-    static long long tiles(const ScanBackwardArgs &a) { return ((long long)a.T + SH::TT - 1) / SH::TT; }
-    static Plan plan(const ScanBackwardArgs &a) {
-        return plan_clusters<BackwardTma>(cols(a), tiles(a),
-                                          (double)kThreads * SH::E * (2 * sizeof(float) + 3 * sizeof(IO)));
-    }
-    static cudaError_t launch(const ScanBackwardArgs &a, int K) {
-        TmaBackwardParams q;
-        if (!row_map<SH>(&q.gate, a.gate, sizeof(float), a.B, a.T, a.C) ||
-            !row_map<SH>(&q.x, a.x, sizeof(IO), a.B, a.T, a.C) || !row_map<SH>(&q.dh, a.dh, sizeof(IO), a.B, a.T, a.C))
-            return cudaErrorInvalidValue;
-        BackwardParams &p = q.b;
-        p.x = a.x; p.dh = a.dh;
-        p.gate = a.gate; p.ckpt = a.ckpt; p.dstate = a.dstate;
-        p.dx = a.dx; p.dgate = a.dgate; p.dstate0 = a.dstate0;
-        p.T = a.T; p.C = a.C;
-        p.blocks = (int)((a.C + SH::CH - 1) / SH::CH);
-        p.K = K;
-        p.steps = (int)((tiles(a) + K - 1) / K);
-        q.err = device_error_word();
-        return launch_cluster<TmaBackwardParams>(kernel, q, cols(a), K, smem(K), a.stream);
-    }
-};
-
-// Whether rows can come by TMA: 16-byte rows and starts (and channels that a lane's vectors and
-// the checkpoints' bulk copies divide), sizes within a tensor map.
-bool tma_rows(long long B, long long T, long long C, size_t elem, std::initializer_list<const void *> in,
-              std::initializer_list<const void *> out) {
-    if (C * elem % 16 || C * 4 % 16 || T * C * 4 >= (1ll << 40)) return false;
-    for (const void *q : in)
-        if (reinterpret_cast<uintptr_t>(q) % 16) return false;
-    for (const void *q : out)
-        if (reinterpret_cast<uintptr_t>(q) % 8) return false;
-    return true;
-}
 
 // Channels a thread: the widest vectors that the rows' length and the tensors' starts allow.
 template <typename IO>
@@ -1456,13 +720,6 @@ int vector_width(long long C, std::initializer_list<const void *> io, std::initi
     return 1;
 }
 
-// The wide shape, or the narrow one where it gives enough more parallelism.
-template <typename Wide, typename Narrow, typename Args>
-cudaError_t launch_best(const Args &a) {
-    const Plan w = Wide::plan(a), n = Narrow::plan(a);
-    return n.cost < 0.9 * w.cost ? Narrow::launch(a, n.K) : Wide::launch(a, w.K);
-}
-
 template <typename IO, int V, bool BLEND, bool PACKED>
 cudaError_t forward_v(const ScanArgs &a) {
     constexpr int E = sizeof(IO) == 2 && V > 1 ? 32 : 16, STAGES = sizeof(IO) == 2 ? 2 : 3;
@@ -1474,18 +731,8 @@ cudaError_t forward_flags(const ScanArgs &a) {
     if (a.codes) return a.blend ? forward_v<IO, V, true, true>(a) : forward_v<IO, V, false, true>(a);
     return a.blend ? forward_v<IO, V, true, false>(a) : forward_v<IO, V, false, false>(a);
 }
-template <typename IO, bool BLEND, bool PACKED>
-cudaError_t forward_tma(const ScanArgs &a) {
-    constexpr int E = sizeof(IO) == 2 ? 32 : 16, STAGES = sizeof(IO) == 2 ? 2 : 3;
-    return launch_best<ForwardTma<IO, TmaShape<2, E>, STAGES, BLEND, PACKED>,
-                       ForwardTma<IO, TmaShape<1, E>, STAGES, BLEND, PACKED>>(a);
-}
 template <typename IO>
 cudaError_t forward_io(const ScanArgs &a) {
-    if (tma_rows(a.B, a.T, a.C, sizeof(IO), {a.x, a.gate}, {a.h, a.ckpt, a.state_in, a.state_out})) {
-        if (a.codes) return a.blend ? forward_tma<IO, true, true>(a) : forward_tma<IO, false, true>(a);
-        return a.blend ? forward_tma<IO, true, false>(a) : forward_tma<IO, false, false>(a);
-    }
     const int V = vector_width<IO>(a.C, {a.x, a.h}, {a.gate, a.ckpt});
     return V == 4 ? forward_flags<IO, 4>(a) : V == 2 ? forward_flags<IO, 2>(a) : forward_flags<IO, 1>(a);
 }
@@ -1495,15 +742,8 @@ cudaError_t backward_v(const ScanBackwardArgs &a) {
     constexpr int E = sizeof(IO) == 2 && V > 1 ? 16 : 8, STAGES = sizeof(IO) == 2 ? 2 : 3;
     return launch_best<Backward<IO, Shape<V, 16, E>, STAGES, BLEND>, Backward<IO, Shape<V, 4, E>, STAGES, BLEND>>(a);
 }
-template <typename IO, bool BLEND>
-cudaError_t backward_tma(const ScanBackwardArgs &a) {
-    constexpr int STAGES = sizeof(IO) == 2 ? 3 : 2;
-    return launch_best<BackwardTma<IO, TmaShape<2, 16>, STAGES, BLEND>, BackwardTma<IO, TmaShape<1, 16>, STAGES, BLEND>>(a);
-}
 template <typename IO>
 cudaError_t backward_io(const ScanBackwardArgs &a) {
-    if (tma_rows(a.B, a.T, a.C, sizeof(IO), {a.x, a.gate, a.dh, a.ckpt}, {a.dx, a.dgate}))
-        return a.blend ? backward_tma<IO, true>(a) : backward_tma<IO, false>(a);
     const int V = vector_width<IO>(a.C, {a.x, a.dh, a.dx}, {a.gate, a.ckpt, a.dgate});
     if (V == 4) return a.blend ? backward_v<IO, 4, true>(a) : backward_v<IO, 4, false>(a);
     if (V == 2) return a.blend ? backward_v<IO, 2, true>(a) : backward_v<IO, 2, false>(a);
@@ -1512,10 +752,12 @@ cudaError_t backward_io(const ScanBackwardArgs &a) {
 
 }  // namespace
 
-size_t scan_codes_bytes(int T) { return sizeof(int) * (((size_t)T + 31) / 32 * 32); }
+// The codes are read in whole tiles of rows.
+constexpr int kCodeRows = 256;
+size_t scan_codes_bytes(int T) { return sizeof(int) * (((size_t)T + kCodeRows - 1) / kCodeRows * kCodeRows); }
 
 cudaError_t launch_scan_rows(const ScanArgs &a, const int *cu, int N, int *codes, float *zero_state) {
-    const int padded = (a.T + 31) / 32 * 32, row_blocks = (padded + 255) / 256;
+    const int padded = (a.T + kCodeRows - 1) / kCodeRows * kCodeRows, row_blocks = (padded + 255) / 256;
     timer_begin(a.stream);
     scan_rows_kernel<<<(unsigned)row_blocks + (unsigned)N, 256, 0, a.stream>>>(a.T, padded, row_blocks, N, a.C, cu,
                                                                                codes, zero_state, device_error_word());
@@ -1525,10 +767,12 @@ cudaError_t launch_scan_rows(const ScanArgs &a, const int *cu, int N, int *codes
 }
 
 cudaError_t launch_scan(const ScanArgs &a) {
+    if (scan_tma_takes(a)) return launch_scan_tma(a);
     return a.dtype == LA_BF16 ? forward_io<__nv_bfloat16>(a) : forward_io<float>(a);
 }
 
 cudaError_t launch_scan_backward(const ScanBackwardArgs &a) {
+    if (scan_tma_takes(a)) return launch_scan_backward_tma(a);
     return a.dtype == LA_BF16 ? backward_io<__nv_bfloat16>(a) : backward_io<float>(a);
 }
 

@@ -1,0 +1,792 @@
+// scan_tma.cu -- the gated linear recurrence (scan.cu) for rows that TMA can take: rows and
+// starts on 16 bytes.  The same cut of the time axis into runs (P, H), with other means.
+//
+// A tile is 8 S rows of 32 V channels; of the CTA's eight warps each walks S of them, each lane V
+// neighbouring channels (as packed fp32 pairs for V = 2), so no shuffle is needed, and sequence
+// starts and the end of the rows are decided for whole warps.  A step:
+//
+//   walk 1          a warp takes its rows of the tile to registers and forms (P, H)
+//   fold            one barrier; then every thread folds the eight runs of its channels itself:
+//                   what lies in front of its warp, and the whole tile.  The barrier also says
+//                   that all warps have taken their rows: one thread asks TMA for the tile STAGES
+//                   steps on, a box of gates, one of x (and of dh), into the same stage
+//   meet (K > 1)    the K CTAs of a cluster, which hold consecutive tiles, send their tile's run
+//                   to each other by st.async, whose bytes complete the receiver's barrier
+//   walk 2          from the state in front of its rows each warp walks them again and stores
+//
+// What bounds it: HBM where there are columns for every SM (B2 T32768 C2048 bf16, 128 CTAs of 32
+// channels); a CTA's step is a chain of latencies (barrier, shared-memory reads, fold), so with
+// few columns the time axis goes over K CTAs and walk 1 of the next step comes before walk 2 of
+// this one (AHEAD): the runs travel meanwhile, and the chain of one step fills that of the other.
+#include "scan_util.cuh"
+#include "tmap.cuh"
+
+#include <cmath>
+#include <initializer_list>
+
+namespace la {
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kSlots = 4;                      // steps whose runs can be on their way between ranks
+
+// V neighbouring channels of one lane, as one (V = 1) or packed (V = 2) fp32 operand.
+template <int V>
+struct Lane;
+template <>
+struct Lane<1> {
+    float v;
+    static __device__ __forceinline__ Lane all(float x) { return {x}; }
+    static __device__ __forceinline__ Lane load(const float *p) { return {*p}; }
+    __device__ __forceinline__ void store(float *p) const { *p = v; }
+    __device__ __forceinline__ void store(__nv_bfloat16 *p) const { *p = __float2bfloat16_rn(v); }
+};
+template <>
+struct Lane<2> {
+    unsigned long long v;
+    static __device__ __forceinline__ Lane make(float a, float b) {
+        Lane r;
+        asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+        return r;
+    }
+    static __device__ __forceinline__ Lane all(float x) { return make(x, x); }
+    __device__ __forceinline__ float2 both() const {
+        float2 r;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+        return r;
+    }
+    static __device__ __forceinline__ Lane load(const float *p) {
+        const float2 f = *reinterpret_cast<const float2 *>(p);
+        return make(f.x, f.y);
+    }
+    __device__ __forceinline__ void store(float *p) const { *reinterpret_cast<float2 *>(p) = both(); }
+    __device__ __forceinline__ void store(__nv_bfloat16 *p) const {
+        const float2 f = both();
+        *reinterpret_cast<uint32_t *>(p) = ptx::pack_bf16x2(f.x, f.y);
+    }
+};
+__device__ __forceinline__ Lane<1> fma(Lane<1> a, Lane<1> b, Lane<1> c) { return {fmaf(a.v, b.v, c.v)}; }
+__device__ __forceinline__ Lane<1> mul(Lane<1> a, Lane<1> b) { return {a.v * b.v}; }
+__device__ __forceinline__ Lane<1> add(Lane<1> a, Lane<1> b) { return {a.v + b.v}; }
+__device__ __forceinline__ Lane<2> fma(Lane<2> a, Lane<2> b, Lane<2> c) {
+    Lane<2> r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ Lane<2> mul(Lane<2> a, Lane<2> b) {
+    Lane<2> r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ Lane<2> add(Lane<2> a, Lane<2> b) {
+    Lane<2> r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+// (1 - a) x with one rounding of the exact x - a x
+template <int V>
+__device__ __forceinline__ Lane<V> blended(Lane<V> a, Lane<V> x) {
+    return fma(mul(a, Lane<V>::all(-1.f)), x, x);
+}
+template <int V>
+__device__ __forceinline__ Lane<V> sub(Lane<V> a, Lane<V> b) {
+    return fma(b, Lane<V>::all(-1.f), a);
+}
+
+__device__ __forceinline__ Lane<1> pick(bool c, Lane<1> a, Lane<1> b) { return {c ? a.v : b.v}; }
+__device__ __forceinline__ Lane<2> pick(bool c, Lane<2> a, Lane<2> b) {
+    Lane<2> r;
+    r.v = c ? a.v : b.v;
+    return r;
+}
+
+// A lane's values as they lie in memory (half the registers for bf16), widened where used.
+template <typename IO, int V>
+struct Raw;
+template <int V>
+struct Raw<float, V> {
+    Lane<V> v;
+    __device__ __forceinline__ void load(const float *p) { v = Lane<V>::load(p); }
+    __device__ __forceinline__ void zero() { v = Lane<V>::all(0.f); }
+    __device__ __forceinline__ Lane<V> wide() const { return v; }
+};
+template <>
+struct Raw<__nv_bfloat16, 1> {
+    uint16_t v;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { v = *reinterpret_cast<const uint16_t *>(p); }
+    __device__ __forceinline__ void zero() { v = 0; }
+    __device__ __forceinline__ Lane<1> wide() const { return {__uint_as_float((uint32_t)v << 16)}; }
+};
+template <>
+struct Raw<__nv_bfloat16, 2> {
+    uint32_t v;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { v = *reinterpret_cast<const uint32_t *>(p); }
+    __device__ __forceinline__ void zero() { v = 0; }
+    __device__ __forceinline__ Lane<2> wide() const {   // bf16 -> fp32: the high half
+        return Lane<2>::make(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+    }
+};
+
+// (P, H) of a run of rows, one lane's channels.
+template <int V>
+struct alignas(8 * V) Run {
+    Lane<V> P, H;
+    static __device__ __forceinline__ Run none() { return {Lane<V>::all(1.f), Lane<V>::all(0.f)}; }
+};
+// To shared memory of CTA `rank` of the cluster; the bytes count towards its barrier `bar` (both
+// given by this CTA's own addresses).
+__device__ __forceinline__ uint32_t of_rank(uint32_t addr, uint32_t rank) {
+    uint32_t to;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(addr), "r"(rank));
+    return to;
+}
+__device__ __forceinline__ void send(uint32_t addr, uint32_t bar, uint32_t rank, const Run<1> &r) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(
+                     of_rank(addr, rank)),
+                 "f"(r.P.v), "f"(r.H.v), "r"(of_rank(bar, rank))
+                 : "memory");
+}
+__device__ __forceinline__ void send(uint32_t addr, uint32_t bar, uint32_t rank, const Run<2> &r) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b64 [%0], {%1, %2}, [%3];" ::"r"(
+                     of_rank(addr, rank)),
+                 "l"(r.P.v), "l"(r.H.v), "r"(of_rank(bar, rank))
+                 : "memory");
+}
+__device__ __forceinline__ void send(uint32_t addr, uint32_t bar, uint32_t rank, int v) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.s32 [%0], %1, [%2];" ::"r"(of_rank(addr, rank)),
+                 "r"(v), "r"(of_rank(bar, rank))
+                 : "memory");
+}
+
+struct TmaScanParams {
+    CUtensorMap gate, x;     // [B][T][C], boxes of a tile: TT rows x CH channels
+    ScanParams s;
+    unsigned *err;
+};
+struct TmaBackwardParams {
+    CUtensorMap gate, x, dh;
+    BackwardParams b;
+    unsigned *err;
+};
+
+// Shape: V channels a lane, E elements a thread.
+template <int V_, int E_>
+struct TmaShape {
+    static constexpr int V = V_, E = E_, S = E / V, CH = 32 * V, TT = kWarps * S;
+    static_assert(TT <= 256 && S <= 32, "a box has at most 256 rows; a warp's row codes fit its lanes");
+};
+constexpr uint32_t whole(uint32_t n) { return (n + 127) / 128 * 128; }
+
+// One stage of the ring: the tile's gates, x (dh), then packed batches' row codes or the
+// backward pass's checkpoint rows (one for each 32 rows).
+template <typename IO, typename SH>
+struct ScanStage {
+    static constexpr uint32_t kGate = SH::TT * SH::CH * sizeof(float), kX = SH::TT * SH::CH * sizeof(IO);
+    static constexpr uint32_t bytes(bool packed) { return whole(kGate + kX + (packed ? SH::TT * 4 : 0)); }
+};
+template <typename IO, typename SH>
+struct BackwardStage {
+    static constexpr uint32_t kGate = SH::TT * SH::CH * sizeof(float), kX = SH::TT * SH::CH * sizeof(IO);
+    static constexpr uint32_t kKept = kGate + 2 * kX;
+    static constexpr int kSpans = SH::TT / kScanCheckpoint;
+    static constexpr uint32_t bytes() { return whole(kKept + kSpans * SH::CH * sizeof(float)); }
+};
+
+// Shared memory: the ring of stages, then this, then (on 16 bytes) Run slot[kSlots][K][32].
+template <int V, int STAGES>
+struct Exchange {
+    Run<V> warp[2][kWarps][32];   // by the step's parity
+    Lane<V> back[2][kWarps][32];  // backward pass: M
+    uint64_t full[STAGES];
+    uint64_t met[kSlots];         // the step's runs of all ranks are here
+    int reset[2][kWarps];         // packed: a sequence starts in the warp's rows
+    int slot_reset[kSlots][kMaxCluster];
+    int abort;
+};
+template <int V, int STAGES>
+constexpr size_t exchange_bytes() { return (sizeof(Exchange<V, STAGES>) + 15) / 16 * 16; }
+
+// Barriers and the cluster's start; the whole CTA.
+template <int V, int STAGES>
+__device__ __forceinline__ void start_exchange(Exchange<V, STAGES> *ex, int K, int askers) {
+    const int tid = threadIdx.x;
+    if (tid < STAGES) ptx::mbar_init(&ex->full[tid], askers);
+    if (tid < kSlots) ptx::mbar_init(&ex->met[tid], 1);
+    if (tid == 0) ex->abort = 0;
+    ptx::fence_mbar_init();
+    if (K > 1) {   // every CTA of the cluster runs before the first store to its shared memory
+        cluster_arrive();
+        cluster_wait();
+    } else {
+        __syncthreads();
+    }
+}
+// The end of the whole CTA.  After a wait that ran out, the copies still in flight get 10 ms to
+// land before the block's shared memory goes; and no CTA may leave while another one's store to
+// it is in flight.
+template <int V, int STAGES>
+__device__ __forceinline__ void end_exchange(Exchange<V, STAGES> *ex, int K) {
+    if (*(volatile int *)&ex->abort)
+        for (int i = 0; i < 1000; ++i) __nanosleep(10000);
+    if (K > 1) {
+        cluster_arrive();
+        cluster_wait();
+    }
+}
+
+// The tile's run to every rank, one rank a warp at a time.
+// A slot is used again kSlots = 4 steps later.  Its sender then has this CTA's run of at least two
+// steps before, which this CTA sent after it had read the slot.
+template <int V, int STAGES, bool RESETS>
+__device__ __forceinline__ void send_run(Exchange<V, STAGES> *ex, Run<V> *slots, int step, int K, int rank,
+                                         const Run<V> &all, bool reset) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slot = step % kSlots;
+    const uint32_t at = ptx::smem_u32(slots + ((size_t)slot * K + rank) * 32 + lane);
+    const uint32_t bar = ptx::smem_u32(&ex->met[slot]);
+    for (int to = warp; to < K; to += kWarps) {
+        send(at, bar, to, all);
+        if (RESETS && lane == 0) send(ptx::smem_u32(&ex->slot_reset[slot][rank]), bar, to, (int)reset);
+    }
+    if (threadIdx.x == 0)
+        ptx::mbar_arrive_expect_tx(&ex->met[slot], K * (32 * (int)sizeof(Run<V>) + (RESETS ? 4 : 0)));
+}
+// All ranks' runs of a step: the state in front of this rank's tile, and `run` behind all tiles.
+template <int V, int STAGES, bool RESETS>
+__device__ __forceinline__ Lane<V> meet(Exchange<V, STAGES> *ex, const Run<V> *slots, int step, int K, int rank,
+                                        Lane<V> &run, unsigned *err) {
+    const int lane = threadIdx.x & 31, slot = step % kSlots;
+    ptx::mbar_wait(&ex->met[slot], (step / kSlots) & 1, &ex->abort, err);
+    Lane<V> in = run;
+    for (int r = 0; r < K; ++r) {
+        if (r == rank) in = run;
+        const Run<V> e = slots[((size_t)slot * K + r) * 32 + lane];
+        run = (RESETS && ex->slot_reset[slot][r]) ? e.H : fma(e.P, run, e.H);
+    }
+    return in;
+}
+
+// A warp's rows in registers, from walk 1 to walk 2.
+template <typename IO, typename SH, bool PACKED>
+struct Rows {
+    Lane<SH::V> a[SH::S];
+    Raw<IO, SH::V> x[SH::S];
+    Run<SH::V> front;       // the rows of the tile in front of the warp's
+    Run<SH::V> tile;
+    bool front_reset, tile_reset;
+    // packed: the row code of row `lane`; bits of the rows that are a sequence's, its first, its last
+    int code;
+    uint32_t held, first, last;
+};
+
+template <typename IO, typename SH, int STAGES, bool BLEND, bool PACKED, bool AHEAD>
+__global__ void __launch_bounds__(kThreads, AHEAD ? 1 : 2) scan_tma_kernel(const __grid_constant__ TmaScanParams q) {
+    constexpr int V = SH::V, S = SH::S, CH = SH::CH, TT = SH::TT;
+    using L = Lane<V>;
+    using St = ScanStage<IO, SH>;
+    constexpr uint32_t kStage = St::bytes(PACKED);
+    extern __shared__ __align__(128) unsigned char ring[];
+    auto *ex = reinterpret_cast<Exchange<V, STAGES> *>(ring + (size_t)STAGES * kStage);
+    auto *slots = reinterpret_cast<Run<V> *>(ring + (size_t)STAGES * kStage + exchange_bytes<V, STAGES>());
+    const ScanParams &p = q.s;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int K = p.K, rank = blockIdx.x % K;
+    const long long col = blockIdx.x / K;
+    const int b = (int)(col / p.blocks);
+    const int cb = (int)(col % p.blocks) * CH, c0 = cb + lane * V;
+    const bool act = c0 < p.C;
+    const long long T = p.T, C = p.C;
+    start_exchange(ex, K, 2);
+    auto tile_row = [&](int step) { return ((long long)step * K + rank) * TT; };
+
+    // The first lanes of warps 0 and 4 ask for a step's gates and x (asking takes a lane some 200
+    // cycles for a box, and its warp with it).
+    const int asks = lane == 0 ? (warp == 0 ? 0 : warp == 4 ? 1 : -1) : -1;
+    auto fetch = [&](int step) {
+        const long long t0 = tile_row(step);
+        if (asks < 0 || step >= p.steps || t0 >= T) return;
+        const uint32_t to = ptx::smem_u32(ring + (size_t)(step % STAGES) * kStage);
+        uint64_t *bar = &ex->full[step % STAGES];
+        if (asks == 0) {
+            ptx::mbar_arrive_expect_tx(bar, St::kGate);
+            ptx::tma_load_3d(to, &q.gate, cb, (int)t0, b, bar);
+        } else {
+            ptx::mbar_arrive_expect_tx(bar, St::kX + (PACKED ? TT * 4 : 0));
+            ptx::tma_load_3d(to + St::kGate, &q.x, cb, (int)t0, b, bar);
+            if (PACKED) ptx::bulk_load(to + St::kGate + St::kX, p.codes + t0, TT * 4, bar);
+        }
+    };
+    for (int i = 0; i < STAGES; ++i) fetch(i);
+
+    constexpr uint32_t kAllRows = S == 32 ? ~0u : (1u << S) - 1;
+    int stage = 0;
+    uint32_t parity = 0;
+    using R = Rows<IO, SH, PACKED>;
+    auto next_h = [&](const R &w, int s, L h) {
+        L u = BLEND ? blended(w.a[s], w.x[s].wide()) : w.x[s].wide();
+        if constexpr (PACKED) {   // at a first row a is its h
+            const bool first = w.first >> s & 1;
+            if (BLEND) u = pick(first, L::all(0.f), u);
+            h = pick(first, L::all(1.f), h);
+        }
+        return fma(w.a[s], h, u);
+    };
+    auto walk1 = [&](int step, R &w) {
+        const long long t0 = tile_row(step) + warp * S;
+        Run<V> own = Run<V>::none();
+        bool reset = false;
+        if (tile_row(step) < T) {
+            ptx::mbar_wait(&ex->full[stage], parity, &ex->abort, q.err);
+            unsigned char *at = ring + (size_t)stage * kStage;
+            float *sa = reinterpret_cast<float *>(at) + warp * S * CH + lane * V;
+            IO *sx = reinterpret_cast<IO *>(at + St::kGate) + warp * S * CH + lane * V;
+            if constexpr (PACKED) {
+                // Rows of no sequence get a = 1, x = 0, which leaves the state.  A sequence's first
+                // row starts from its slot of the states, here and now (walk 2 comes when the slot
+                // may be overwritten): the row's h takes its gate's place, to be multiplied by 1.
+                // Done in the ring, row by row, so that the walks hold a choice at each row but no
+                // branch: branches (or a second copy of the walks) cost a warp more than the walk.
+                w.code = lane < S ? reinterpret_cast<const int *>(at + St::kGate + St::kX)[warp * S + lane] : 0;
+                w.held = __ballot_sync(~0u, w.code != 0);
+                w.first = __ballot_sync(~0u, row_first(w.code));
+                w.last = __ballot_sync(~0u, row_last(w.code));
+                reset = w.first != 0;
+                for (uint32_t m = ~w.held & kAllRows; m; m &= m - 1) {
+                    const int s = __ffs(m) - 1;
+                    L::all(1.f).store(sa + s * CH);
+                    L::all(0.f).store(sx + s * CH);
+                }
+                for (uint32_t m = w.first; m; m &= m - 1) {
+                    const int s = __ffs(m) - 1;
+                    const long long seq = row_seq(__shfl_sync(~0u, w.code, s));
+                    Raw<IO, V> x;
+                    x.load(sx + s * CH);
+                    const L a = L::load(sa + s * CH);
+                    L h = BLEND ? blended(a, x.wide()) : x.wide();
+                    if (act && p.state_in) h = fma(a, L::load(p.state_in + seq * C + c0), h);
+                    h.store(sa + s * CH);
+                    L::all(0.f).store(sx + s * CH);
+                }
+                if (w.held != kAllRows || w.first) ptx::fence_async_smem();   // before the ring's next copy
+            }
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                w.a[s] = L::load(sa + s * CH);
+                w.x[s].load(sx + s * CH);
+            }
+            if (++stage == STAGES) stage = 0, parity ^= 1;
+            if (!PACKED && t0 + S > T) {   // rows behind the end: a = 1, x = 0 leaves the state
+#pragma unroll
+                for (int s = 0; s < S; ++s)
+                    if (t0 + s >= T) w.a[s] = L::all(1.f), w.x[s].zero();
+            }
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                own.H = next_h(w, s, own.H);
+                own.P = mul(own.P, w.a[s]);
+            }
+        }
+        const int par = step & 1;
+        ex->warp[par][warp][lane] = own;
+        if (PACKED && lane == 0) ex->reset[par][warp] = reset;
+        __syncthreads();
+        fetch(step + STAGES);
+        w.front = w.tile = Run<V>::none();
+        w.front_reset = w.tile_reset = false;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+            if (i == warp) w.front = w.tile, w.front_reset = w.tile_reset;
+            const Run<V> r = ex->warp[par][i][lane];
+            if (PACKED && ex->reset[par][i]) {
+                w.tile = r, w.tile_reset = true;
+            } else {
+                w.tile.H = fma(r.P, w.tile.H, r.H);
+                w.tile.P = mul(w.tile.P, r.P);
+            }
+        }
+        if (K > 1) send_run<V, STAGES, PACKED>(ex, slots, step, K, rank, w.tile, w.tile_reset);
+    };
+
+    L run = L::all(0.f);
+    if (!PACKED && act && p.state_in) run = L::load(p.state_in + b * C + c0);
+    IO *hb = p.h ? static_cast<IO *>(p.h) + b * T * C + c0 : nullptr;
+    auto walk2 = [&](int step, R &w) {
+        L in = run;
+        if (K > 1) in = meet<V, STAGES, PACKED>(ex, slots, step, K, rank, run, q.err);
+        else run = (PACKED && w.tile_reset) ? w.tile.H : fma(w.tile.P, run, w.tile.H);
+        const long long t0 = tile_row(step) + warp * S;
+        if ((!PACKED && !act) || t0 >= T) return;
+        L h = (PACKED && w.front_reset) ? w.front.H : fma(w.front.P, in, w.front.H);
+        if (p.ckpt && t0 % kScanCheckpoint == 0) {
+            const long long rows = (T + kScanCheckpoint - 1) / kScanCheckpoint;
+            h.store(p.ckpt + (b * rows + t0 / kScanCheckpoint) * C + c0);
+        }
+        if (!hb) return;
+        IO *to = hb + t0 * C;
+        if constexpr (PACKED) {
+            // lanes without channels are still here, for the shuffles
+            const uint32_t stored = act ? w.held : 0;
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                w.a[s] = h = next_h(w, s, h);
+                if (stored >> s & 1) h.store(to);
+                to += C;
+            }
+            for (uint32_t m = w.last; m; m &= m - 1) {   // the last rows' h, to their sequences' states
+                const int last = __ffs(m) - 1;
+                const long long seq = row_seq(__shfl_sync(~0u, w.code, last));
+                L end = w.a[0];
+#pragma unroll
+                for (int s = 1; s < S; ++s) end = pick(s == last, w.a[s], end);
+                if (act) end.store(p.state_out + seq * C + c0);
+            }
+        } else if (t0 + S <= T) {
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                h = next_h(w, s, h);
+                h.store(to);
+                to += C;
+            }
+        } else {
+#pragma unroll 1
+            for (int n = 0; t0 + n < T; ++n) {
+                L a = w.a[0];
+                Raw<IO, V> x = w.x[0];
+#pragma unroll
+                for (int s = 1; s < S; ++s)
+                    if (s == n) a = w.a[s], x = w.x[s];
+                h = fma(a, h, BLEND ? blended(a, x.wide()) : x.wide());
+                h.store(to);
+                to += C;
+            }
+        }
+    };
+    R w;
+    if constexpr (AHEAD) {
+        walk1(0, w);
+        for (int step = 0; step < p.steps; ++step) {
+            R next;
+            if (step + 1 < p.steps) walk1(step + 1, next);
+            walk2(step, w);
+            w = next;
+        }
+    } else {
+        for (int step = 0; step < p.steps; ++step) {
+            walk1(step, w);
+            walk2(step, w);
+        }
+    }
+    if (!PACKED && rank == 0 && warp == 0 && act && p.state_out) run.store(p.state_out + b * C + c0);
+    end_exchange(ex, K);
+}
+
+template <typename IO, typename SH>
+struct BackwardRows {
+    Lane<SH::V> a[SH::S];
+    Raw<IO, SH::V> x[SH::S], d[SH::S];
+    Lane<SH::V> front;            // forwards: the state in front of the warp's rows
+    Run<SH::V> behind, tile;      // backwards: the rows of the tile behind the warp's, and the tile
+};
+
+// Tiles from the last row to the first.  A run of rows acts on m (the next row's a l) as
+// m -> P m + M.  h_{t-1} comes from the checkpoint in front of every 32nd row.
+template <typename IO, typename SH, int STAGES, bool BLEND, bool AHEAD>
+__global__ void __launch_bounds__(kThreads, AHEAD ? 1 : 2)
+scan_backward_tma_kernel(const __grid_constant__ TmaBackwardParams q) {
+    constexpr int V = SH::V, S = SH::S, CH = SH::CH, TT = SH::TT;
+    constexpr int kGroups = kScanCheckpoint / S;   // warps between two checkpoints
+    static_assert(kScanCheckpoint % S == 0 && TT % kScanCheckpoint == 0, "tiles hold whole checkpoint spans");
+    using L = Lane<V>;
+    using St = BackwardStage<IO, SH>;
+    constexpr uint32_t kStage = St::bytes();
+    extern __shared__ __align__(128) unsigned char ring[];
+    auto *ex = reinterpret_cast<Exchange<V, STAGES> *>(ring + (size_t)STAGES * kStage);
+    auto *slots = reinterpret_cast<Run<V> *>(ring + (size_t)STAGES * kStage + exchange_bytes<V, STAGES>());
+    const BackwardParams &p = q.b;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int K = p.K, rank = blockIdx.x % K;
+    const long long col = blockIdx.x / K;
+    const int b = (int)(col / p.blocks);
+    const int cb = (int)(col % p.blocks) * CH, c0 = cb + lane * V;
+    const bool act = c0 < p.C;
+    const long long T = p.T, C = p.C;
+    const long long tiles = (T + TT - 1) / TT, rows = (T + kScanCheckpoint - 1) / kScanCheckpoint;
+    start_exchange(ex, K, 3);
+    // negative (before the first row) at the last steps of some ranks
+    auto tile_row = [&](int step) { return (tiles - 1 - ((long long)step * K + rank)) * TT; };
+
+    const uint32_t kept_bytes = (uint32_t)(C - cb < CH ? C - cb : CH) * sizeof(float);
+    // gates, x, and dh with the checkpoint rows: the first lanes of three warps
+    const int asks = lane == 0 ? (warp == 0 ? 0 : warp == 3 ? 1 : warp == 6 ? 2 : -1) : -1;
+    auto fetch = [&](int step) {
+        const long long t0 = tile_row(step);
+        if (asks < 0 || step >= p.steps || t0 < 0) return;
+        const uint32_t to = ptx::smem_u32(ring + (size_t)(step % STAGES) * kStage);
+        uint64_t *bar = &ex->full[step % STAGES];
+        if (asks == 0) {
+            ptx::mbar_arrive_expect_tx(bar, St::kGate);
+            ptx::tma_load_3d(to, &q.gate, cb, (int)t0, b, bar);
+        } else if (asks == 1) {
+            ptx::mbar_arrive_expect_tx(bar, St::kX);
+            ptx::tma_load_3d(to + St::kGate, &q.x, cb, (int)t0, b, bar);
+        } else {
+            const long long k0 = t0 / kScanCheckpoint;
+            const int spans = rows - k0 < St::kSpans ? (int)(rows - k0) : St::kSpans;
+            ptx::mbar_arrive_expect_tx(bar, St::kX + spans * kept_bytes);
+            ptx::tma_load_3d(to + St::kGate + St::kX, &q.dh, cb, (int)t0, b, bar);
+            for (int i = 0; i < spans; ++i)
+                ptx::bulk_load(to + St::kKept + i * CH * (uint32_t)sizeof(float), p.ckpt + (b * rows + k0 + i) * C + cb,
+                               kept_bytes, bar);
+        }
+    };
+    for (int i = 0; i < STAGES; ++i) fetch(i);
+
+    const bool kept = warp % kGroups == 0;   // the warp's rows start at a checkpoint
+    int stage = 0;
+    uint32_t parity = 0;
+    using R = BackwardRows<IO, SH>;
+    auto walk1 = [&](int step, R &w) {
+        const long long t0 = tile_row(step) + warp * S;
+        Run<V> own = Run<V>::none();
+        L M = L::all(0.f), k = L::all(0.f);
+        if (tile_row(step) >= 0) {
+            ptx::mbar_wait(&ex->full[stage], parity, &ex->abort, q.err);
+            const unsigned char *at = ring + (size_t)stage * kStage;
+            const int o = warp * S * CH + lane * V;
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                w.a[s] = L::load(reinterpret_cast<const float *>(at) + o + s * CH);
+                w.x[s].load(reinterpret_cast<const IO *>(at + St::kGate) + o + s * CH);
+                w.d[s].load(reinterpret_cast<const IO *>(at + St::kGate + St::kX) + o + s * CH);
+            }
+            if (kept && act && t0 < T)
+                k = L::load(reinterpret_cast<const float *>(at + St::kKept) + warp / kGroups * CH + lane * V);
+            if (++stage == STAGES) stage = 0, parity ^= 1;
+            if (t0 + S > T) {
+#pragma unroll
+                for (int s = 0; s < S; ++s)
+                    if (t0 + s >= T) w.a[s] = L::all(1.f), w.x[s].zero(), w.d[s].zero();
+            }
+            // P and H forwards (H from the checkpoint where the warp has one); M is the sum over
+            // the rows of dh times the product of the gates up to the row
+            own.H = k;
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                own.H = fma(w.a[s], own.H, BLEND ? blended(w.a[s], w.x[s].wide()) : w.x[s].wide());
+                own.P = mul(own.P, w.a[s]);
+                M = fma(own.P, w.d[s].wide(), M);
+            }
+        }
+        const int par = step & 1;
+        ex->warp[par][warp][lane] = own;
+        ex->back[par][warp][lane] = M;
+        __syncthreads();
+        fetch(step + STAGES);
+        w.front = k;
+        if (!kept) {
+            const int from = warp / kGroups * kGroups;
+            w.front = ex->warp[par][from][lane].H;
+            for (int i = from + 1; i < warp; ++i) {
+                const Run<V> r = ex->warp[par][i][lane];
+                w.front = fma(r.P, w.front, r.H);
+            }
+        }
+        w.behind = w.tile = Run<V>::none();
+#pragma unroll
+        for (int i = kWarps - 1; i >= 0; --i) {
+            if (i == warp) w.behind = w.tile;
+            const L P = ex->warp[par][i][lane].P;
+            w.tile.H = fma(P, w.tile.H, ex->back[par][i][lane]);
+            w.tile.P = mul(w.tile.P, P);
+        }
+        if (K > 1) send_run<V, STAGES, false>(ex, slots, step, K, rank, w.tile, false);
+    };
+
+    L run = L::all(0.f);
+    if (act && p.dstate) run = L::load(p.dstate + b * C + c0);
+    IO *ob = static_cast<IO *>(p.dx) + b * T * C + c0;
+    float *gb = p.dgate ? p.dgate + b * T * C + c0 : nullptr;
+    auto walk2 = [&](int step, R &w) {
+        L in = run;
+        if (K > 1) in = meet<V, STAGES, false>(ex, slots, step, K, rank, run, q.err);
+        else run = fma(w.tile.P, run, w.tile.H);
+        const long long t0 = tile_row(step) + warp * S;
+        if (!act || t0 < 0 || t0 >= T) return;
+        L before[S], h = w.front, m = fma(w.behind.P, in, w.behind.H);
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            before[s] = h;
+            h = fma(w.a[s], h, BLEND ? blended(w.a[s], w.x[s].wide()) : w.x[s].wide());
+        }
+        auto row = [&](int s, IO *to, float *tg) {
+            const L l = add(w.d[s].wide(), m);
+            m = mul(w.a[s], l);
+            (BLEND ? blended(w.a[s], l) : l).store(to);
+            if (tg) mul(l, BLEND ? sub(before[s], w.x[s].wide()) : before[s]).store(tg);
+        };
+        IO *to = ob + (t0 + S - 1) * C;
+        if (t0 + S <= T && gb) {
+            float *tg = gb + (t0 + S - 1) * C;
+#pragma unroll
+            for (int s = S - 1; s >= 0; --s) {
+                row(s, to, tg);
+                to -= C;
+                tg -= C;
+            }
+        } else {
+#pragma unroll
+            for (int s = S - 1; s >= 0; --s)
+                if (t0 + s < T) row(s, ob + (t0 + s) * C, gb ? gb + (t0 + s) * C : nullptr);
+        }
+    };
+    R w;
+    if constexpr (AHEAD) {
+        walk1(0, w);
+        for (int step = 0; step < p.steps; ++step) {
+            R next;
+            if (step + 1 < p.steps) walk1(step + 1, next);
+            walk2(step, w);
+            w = next;
+        }
+    } else {
+        for (int step = 0; step < p.steps; ++step) {
+            walk1(step, w);
+            walk2(step, w);
+        }
+    }
+    if (rank == 0 && warp == 0 && act && p.dstate0) run.store(p.dstate0 + b * C + c0);
+    end_exchange(ex, K);
+}
+
+// ------------------------------------------------------------------------------- host side
+
+// Row tensors as TMA sees them: [B][T][C] in boxes of TT rows x CH channels.
+template <typename SH, typename IO>
+bool row_map(CUtensorMap *map, const IO *base, long long B, long long T, long long C) {
+    return make_tmap_3d(map, base, sizeof(IO) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                        sizeof(IO), C, T, B, C * sizeof(IO), T * C * sizeof(IO), SH::CH, SH::TT, false);
+}
+
+// BASE and MORE: ns of a CTA's step alone on its SM, and more for each doubling of K (measured:
+// (time of a call with few columns - 6 us) / steps).  RATE: bytes a ns of all CTAs together
+// (measured where the columns fill the SMs).
+template <typename IO, typename SH, int STAGES, bool BLEND, bool PACKED, bool AHEAD, int MOST, int BASE, int MORE, int RATE>
+struct Forward {
+    static constexpr auto kernel = scan_tma_kernel<IO, SH, STAGES, BLEND, PACKED, AHEAD>;
+    static constexpr int kBlock = kThreads, kChannels = SH::CH, kMost = MOST;
+    static constexpr double kTileBytes = (double)SH::TT * SH::CH * (sizeof(float) + 2 * sizeof(IO));
+    static constexpr double kRate = RATE;
+    static double step_ns(int K) { return BASE + MORE * std::log2((double)K); }
+    static size_t smem(int K) {
+        return (size_t)STAGES * ScanStage<IO, SH>::bytes(PACKED) + exchange_bytes<SH::V, STAGES>() +
+               (K > 1 ? (size_t)kSlots * K * 32 * sizeof(Run<SH::V>) : 0);
+    }
+    static long long cols(const ScanArgs &a) { return (long long)a.B * ((a.C + SH::CH - 1) / SH::CH); }
+    static long long tiles(const ScanArgs &a) { return ((long long)a.T + SH::TT - 1) / SH::TT; }
+    static cudaError_t launch(const ScanArgs &a, int K) {
+        TmaScanParams q;
+        if (!row_map<SH>(&q.gate, a.gate, a.B, a.T, a.C) ||
+            !row_map<SH>(&q.x, static_cast<const IO *>(a.x), a.B, a.T, a.C))
+            return cudaErrorInvalidValue;
+        q.s = scan_params<Forward>(a, K);
+        q.err = device_error_word();
+        return launch_cluster<Forward>(q, cols(a), K, a.stream);
+    }
+};
+
+template <typename IO, typename SH, int STAGES, bool BLEND, bool AHEAD, int MOST, int BASE, int MORE, int RATE>
+struct Backward {
+    static constexpr auto kernel = scan_backward_tma_kernel<IO, SH, STAGES, BLEND, AHEAD>;
+    static constexpr int kBlock = kThreads, kChannels = SH::CH, kMost = MOST;
+    static constexpr double kTileBytes = (double)SH::TT * SH::CH * (2 * sizeof(float) + 3 * sizeof(IO));
+    static constexpr double kRate = RATE;
+    static double step_ns(int K) { return BASE + MORE * std::log2((double)K); }
+    static size_t smem(int K) {
+        return (size_t)STAGES * BackwardStage<IO, SH>::bytes() + exchange_bytes<SH::V, STAGES>() +
+               (K > 1 ? (size_t)kSlots * K * 32 * sizeof(Run<SH::V>) : 0);
+    }
+    static long long cols(const ScanBackwardArgs &a) { return (long long)a.B * ((a.C + SH::CH - 1) / SH::CH); }
+    static long long tiles(const ScanBackwardArgs &a) { return ((long long)a.T + SH::TT - 1) / SH::TT; }
+    static cudaError_t launch(const ScanBackwardArgs &a, int K) {
+        TmaBackwardParams q;
+        if (!row_map<SH>(&q.gate, a.gate, a.B, a.T, a.C) ||
+            !row_map<SH>(&q.x, static_cast<const IO *>(a.x), a.B, a.T, a.C) ||
+            !row_map<SH>(&q.dh, static_cast<const IO *>(a.dh), a.B, a.T, a.C))
+            return cudaErrorInvalidValue;
+        q.b = backward_params<Backward>(a, K);
+        q.err = device_error_word();
+        return launch_cluster<Backward>(q, cols(a), K, a.stream);
+    }
+};
+
+// Rows and starts on 16 bytes (a lane's vectors and the checkpoints' copies divide them), outputs
+// on the vectors of a lane, sizes within a tensor map.
+bool rows_fit(long long T, long long C, size_t elem, std::initializer_list<const void *> in,
+              std::initializer_list<const void *> out) {
+    if (C * elem % 16 || C * 4 % 16 || T * C * 4 >= (1ll << 40)) return false;
+    for (const void *q : in)
+        if (reinterpret_cast<uintptr_t>(q) % 16) return false;
+    for (const void *q : out)
+        if (reinterpret_cast<uintptr_t>(q) % 8) return false;
+    return true;
+}
+
+// The variants, of which a call takes the one with the least estimated time:
+//   two CTAs an SM, K = 1, a step after the other: many columns;
+//   one CTA an SM, AHEAD, K = 1 .. 16: few columns, and with a ring of 144 KB and more also the
+//   fastest where 32-channel columns fill the SMs once (B2 T32768 C2048 bf16: 167 us against 172).
+// V = 2 has half the columns and 256-byte gate rows, V = 1 twice the CTAs.
+template <typename IO, bool BLEND, bool PACKED>
+cudaError_t forward(const ScanArgs &a) {
+    if constexpr (sizeof(IO) == 2)
+        return launch_best<Forward<IO, TmaShape<2, 32>, 2, BLEND, PACKED, false, 1, 900, 0, 6400>,
+                           Forward<IO, TmaShape<1, 32>, 2, BLEND, PACKED, false, 1, 1200, 0, 6300>,
+                           Forward<IO, TmaShape<2, 32>, 3, BLEND, PACKED, true, 8, 1250, 50, 6300>,
+                           Forward<IO, TmaShape<1, 32>, 3, BLEND, PACKED, true, 16, 1250, 200, 6500>>(a);
+    else
+        return launch_best<Forward<IO, TmaShape<2, 16>, 3, BLEND, PACKED, false, 1, 670, 0, 6400>,
+                           Forward<IO, TmaShape<1, 16>, 3, BLEND, PACKED, false, 1, 680, 0, 6300>,
+                           Forward<IO, TmaShape<2, 32>, 3, BLEND, PACKED, true, 8, 1400, 60, 6200>,
+                           Forward<IO, TmaShape<1, 32>, 3, BLEND, PACKED, true, 16, 1450, 140, 6300>>(a);
+}
+template <typename IO>
+cudaError_t forward_io(const ScanArgs &a) {
+    if (a.codes) return a.blend ? forward<IO, true, true>(a) : forward<IO, false, true>(a);
+    return a.blend ? forward<IO, true, false>(a) : forward<IO, false, false>(a);
+}
+
+// The backward pass fills HBM best with two CTAs an SM and one step after the other (B2 T32768
+// C2048 bf16, K = 2: 329 us; one CTA an SM and AHEAD: 380 to 410, with more spread, although each
+// of its CTAs is faster alone), and has few columns go AHEAD.
+template <typename IO, bool BLEND>
+cudaError_t backward(const ScanBackwardArgs &a) {
+    if constexpr (sizeof(IO) == 2)
+        return launch_best<Backward<IO, TmaShape<2, 16>, 3, BLEND, false, 4, 1130, 150, 5900>,
+                           Backward<IO, TmaShape<2, 32>, 3, BLEND, true, 8, 1930, 30, 5000>,
+                           Backward<IO, TmaShape<1, 32>, 3, BLEND, true, 16, 2100, 250, 4600>>(a);
+    else
+        return launch_best<Backward<IO, TmaShape<2, 16>, 2, BLEND, false, 4, 1180, 150, 6000>,
+                           Backward<IO, TmaShape<2, 16>, 4, BLEND, true, 8, 1300, 60, 5300>,
+                           Backward<IO, TmaShape<1, 16>, 4, BLEND, true, 16, 1300, 100, 4800>>(a);
+}
+template <typename IO>
+cudaError_t backward_io(const ScanBackwardArgs &a) {
+    return a.blend ? backward<IO, true>(a) : backward<IO, false>(a);
+}
+
+}  // namespace
+
+bool scan_tma_takes(const ScanArgs &a) {
+    return rows_fit(a.T, a.C, a.dtype == LA_BF16 ? 2 : 4, {a.x, a.gate}, {a.h, a.ckpt, a.state_in, a.state_out});
+}
+bool scan_tma_takes(const ScanBackwardArgs &a) {
+    return rows_fit(a.T, a.C, a.dtype == LA_BF16 ? 2 : 4, {a.x, a.gate, a.dh, a.ckpt},
+                    {a.dx, a.dgate, a.dstate, a.dstate0});
+}
+cudaError_t launch_scan_tma(const ScanArgs &a) {
+    return a.dtype == LA_BF16 ? forward_io<__nv_bfloat16>(a) : forward_io<float>(a);
+}
+cudaError_t launch_scan_backward_tma(const ScanBackwardArgs &a) {
+    return a.dtype == LA_BF16 ? backward_io<__nv_bfloat16>(a) : backward_io<float>(a);
+}
+
+}  // namespace la

@@ -1,0 +1,174 @@
+// scan_util.cuh -- what the two forms of the gated linear recurrence share: row codes of packed
+// batches, the exchange through distributed shared memory, and the choice of the cluster width.
+#pragma once
+
+#include "la_internal.cuh"
+#include "ptx.cuh"
+
+#include <atomic>
+
+namespace la {
+namespace {
+
+constexpr int kMaxCluster = 16;
+
+// Row codes of a packed batch (one int32 a row, from scan_rows_kernel): 0 for a row of no
+// sequence, else 4 (sequence + 1) + 2 (its last row) + 1 (its first row).
+__device__ __forceinline__ bool row_first(int code) { return code & 1; }
+__device__ __forceinline__ bool row_last(int code) { return code & 2; }
+__device__ __forceinline__ long long row_seq(int code) { return (code >> 2) - 1; }
+
+struct ScanParams {
+    const void *x;
+    const float *gate;
+    const float *state_in;   // [B or N, C]; nullptr: zeros
+    float *state_out;        // [B or N, C]; nullptr: not kept.  May be state_in.
+    void *h;                 // nullptr: not kept
+    float *ckpt;             // [B, ceil(T / 32), C]; nullptr: not kept
+    const int *codes;        // packed: [T rounded up to kCodeRows]
+    long long T, C;
+    int blocks;              // channel blocks of one batch row
+    int K;                   // CTAs of a cluster
+    int steps;               // tiles each CTA walks
+};
+
+struct BackwardParams {
+    const void *x, *dh;
+    const float *gate, *ckpt, *dstate;   // dstate: nullptr for zeros
+    void *dx;
+    float *dgate, *dstate0;              // dstate0: nullptr: not kept
+    long long T, C;
+    int blocks, K, steps;
+};
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
+// ------------------------------------------------------------------------------- host side
+
+// How many clusters of K CTAs of launcher L's kernel run at once (asked once a process; the same
+// on every B200); 0 where the kernel cannot have that width.
+template <typename L>
+int clusters_at_once(int K) {
+    static std::atomic<int> known[kMaxCluster + 1];   // the answer plus one
+    int n = known[K].load(std::memory_order_relaxed) - 1;
+    if (n >= 0) return n;
+    n = 0;
+    constexpr auto kernel = L::kernel;
+    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::smem(K));
+    if (err == cudaSuccess && K > 8) err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (err == cudaSuccess) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim = {(unsigned)K, 1, 1};
+        cfg.gridDim = dim3(K * 1024);
+        cfg.blockDim = dim3(L::kBlock);
+        cfg.dynamicSmemBytes = L::smem(K);
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        err = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+    }
+    if (err != cudaSuccess) {
+        (void)cudaGetLastError();
+        n = 0;
+    }
+    known[K].store(n + 1, std::memory_order_relaxed);
+    return n;
+}
+
+// The estimated time, in ns, of `cols` columns (batch rows x channel blocks) of `tiles` tiles
+// with clusters of K: a CTA's step takes L::step_ns(K) where HBM keeps up (half as much again
+// where two CTAs share an SM), and all CTAs together move at most L::kRate bytes a ns; clusters that
+// do not run at once take further waves.
+template <typename L>
+double estimate(long long cols, long long tiles, int K) {
+    const int fit = clusters_at_once<L>(K);
+    if (fit < 1) return 1e300;
+    const long long waves = (cols + fit - 1) / fit;
+    const double active = (double)(cols < fit ? cols : fit) * K, crowd = active > 148 ? active / 148 : 1.0;
+    const double step = L::step_ns(K) * (0.5 + 0.5 * crowd), fed = L::kTileBytes * active / L::kRate;
+    return waves * ((tiles + K - 1) / K + 1) * (step > fed ? step : fed);
+}
+
+template <typename L, typename P>
+cudaError_t launch_cluster(const P &p, long long cols, int K, cudaStream_t stream) {
+    constexpr auto kernel = L::kernel;
+    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::smem(K));
+    if (err == cudaSuccess && K > 8) err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (err != cudaSuccess) return err;
+    if (cols > INT32_MAX / K) return cudaErrorInvalidConfiguration;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim = {(unsigned)K, 1, 1};
+    cfg.gridDim = dim3((unsigned)(cols * K));
+    cfg.blockDim = dim3(L::kBlock);
+    cfg.dynamicSmemBytes = L::smem(K);
+    cfg.stream = stream;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    timer_begin(stream);
+    err = cudaLaunchKernelEx(&cfg, kernel, p);
+    timer_end(stream);
+    note_launches(1);
+    return err != cudaSuccess ? err : cudaGetLastError();
+}
+
+// The best cluster width of a launcher.
+struct Plan {
+    int K = 1;
+    double ns = 1e300;
+};
+template <typename L, typename Args>
+Plan plan(const Args &a) {
+    Plan best;
+    const long long cols = L::cols(a), tiles = L::tiles(a);
+    for (int K = 1; K <= L::kMost; K *= 2) {
+        if (K > 1 && K >= 2 * tiles) break;
+        const double ns = estimate<L>(cols, tiles, K);
+        if (ns < best.ns) best.ns = ns, best.K = K;
+    }
+    return best;
+}
+// The launcher with the least estimated time.
+template <typename... Ls, typename Args>
+cudaError_t launch_best(const Args &a) {
+    const Plan plans[] = {plan<Ls>(a)...};
+    int best = 0;
+    for (int i = 1; i < (int)sizeof...(Ls); ++i)
+        if (plans[i].ns < plans[best].ns) best = i;
+    cudaError_t err = cudaErrorInvalidConfiguration;
+    int i = 0;
+    ((i++ == best ? (void)(err = Ls::launch(a, plans[best].K)) : (void)0), ...);
+    return err;
+}
+
+// The parameters of one call that the launchers have in common.
+template <typename L>
+ScanParams scan_params(const ScanArgs &a, int K) {
+    ScanParams p;
+    p.x = a.x; p.gate = a.gate;
+    p.state_in = a.state_in; p.state_out = a.state_out;
+    p.h = a.h; p.ckpt = a.ckpt; p.codes = a.codes;
+    p.T = a.T; p.C = a.C;
+    p.blocks = (int)((a.C + L::kChannels - 1) / L::kChannels);
+    p.K = K;
+    p.steps = (int)((L::tiles(a) + K - 1) / K);
+    return p;
+}
+template <typename L>
+BackwardParams backward_params(const ScanBackwardArgs &a, int K) {
+    BackwardParams p;
+    p.x = a.x; p.dh = a.dh;
+    p.gate = a.gate; p.ckpt = a.ckpt; p.dstate = a.dstate;
+    p.dx = a.dx; p.dgate = a.dgate; p.dstate0 = a.dstate0;
+    p.T = a.T; p.C = a.C;
+    p.blocks = (int)((a.C + L::kChannels - 1) / L::kChannels);
+    p.K = K;
+    p.steps = (int)((L::tiles(a) + K - 1) / K);
+    return p;
+}
+
+}  // namespace
+}  // namespace la

@@ -170,7 +170,7 @@ LENGTHS = [[5], [1], [0, 0, 3], [65, 0, 1, 64, 130, 63, 200, 2], [1] * 40, [300,
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("lengths", LENGTHS)
-@pytest.mark.parametrize("C", [64, 50, 7])
+@pytest.mark.parametrize("C", [64, 40, 50, 7])
 @pytest.mark.parametrize("init", [False, True])
 def test_scan_varlen_matches_oracle(la, dtype, lengths, C, init):
     T, N = sum(lengths), len(lengths)

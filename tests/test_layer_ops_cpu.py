@@ -48,7 +48,7 @@ def test_scan_refusals(la):
 def test_workspace_sizes(la):
     lib = la.library()
     assert lib.la_linear_scan_varlen_workspace_size(0) == 0
-    assert lib.la_linear_scan_varlen_workspace_size(33) == 4 * 64
+    assert lib.la_linear_scan_varlen_workspace_size(33) == 4 * 256
     assert lib.la_linear_scan_backward_workspace_size(2, 65, 100) == 4 * 2 * 3 * 100
     assert lib.la_linear_scan_backward_workspace_size(2, 0, 100) == 0
     assert lib.la_rms_norm_backward_workspace_size(1, 1, 3, 100) == 4 * 3 * 100
