@@ -27,6 +27,7 @@
 #include "la_internal.cuh"
 #include "vec.cuh"
 
+#include <atomic>
 #include <cuda_fp8.h>
 
 namespace la {
@@ -43,7 +44,7 @@ struct NormParams {
     float *scales;    // [rows, C / group]
     long long rows;   // B * H * T
     int H, T, C;
-    int group;        // 8-bit output: columns a scale
+    FastDiv byT, byH;
     float eps, inv_c;
 };
 
@@ -54,49 +55,45 @@ struct NormBackwardParams {
     float *partial;   // [blocks, C]
     long long rows;
     int H, T, C;
+    FastDiv byT, byH;
     float eps, inv_c;
 };
 
 // Row of y for row i of x: (b, head, t) -> (b, t, head).
-__device__ __forceinline__ long long out_row(long long i, int H, int T) {
-    if (H == 1) return i;
-    const long long bh = i / T, t = i - bh * T, b = bh / H;
-    return (b * T + t) * H + (bh - b * H);
+template <typename P>
+__device__ __forceinline__ long long out_row(const P &p, long long i) {
+    if (p.H == 1) return i;
+    if (p.rows <= INT32_MAX) {
+        const unsigned n = (unsigned)i, bh = p.byT(n), t = n - bh * p.T, b = p.byH(bh);
+        return ((long long)b * p.T + t) * p.H + (bh - b * p.H);
+    }
+    const long long bh = i / p.T, t = i - bh * p.T, b = bh / p.H;
+    return (b * p.T + t) * p.H + (bh - b * p.H);
 }
 
-// Sum and maximum over the NT threads of a row, the same in each of them.  NT > 32: one row a
-// CTA; `box` is one of two alternating areas, so a row's reads never meet the next row's writes.
-template <int NT>
-__device__ __forceinline__ float2 row_sum(float2 v, float2 *box) {
+// For each of ROWS rows: x summed over the NT threads of the row, y summed or (MAX) its maximum,
+// the same in each of them.  NT > 32: a row has a whole CTA; `box` is one of two alternating
+// areas, so the reads of a turn never meet the next turn's writes.
+template <int NT, int ROWS, bool MAX>
+__device__ __forceinline__ void row_sums(float2 (&v)[ROWS], float2 (*box)[NT > 32 ? NT / 32 : 1]) {
+    auto join = [](float2 a, float2 b) { return make_float2(a.x + b.x, MAX ? fmaxf(a.y, b.y) : a.y + b.y); };
 #pragma unroll
-    for (int off = (NT < 32 ? NT : 32) / 2; off > 0; off >>= 1) {
-        v.x += __shfl_xor_sync(~0u, v.x, off);
-        v.y += __shfl_xor_sync(~0u, v.y, off);
-    }
-    if (NT > 32) {
-        if ((threadIdx.x & 31) == 0) box[threadIdx.x >> 5] = v;
+    for (int off = (NT < 32 ? NT : 32) / 2; off > 0; off >>= 1)
+#pragma unroll
+        for (int q = 0; q < ROWS; ++q)
+            v[q] = join(v[q], make_float2(__shfl_xor_sync(~0u, v[q].x, off), __shfl_xor_sync(~0u, v[q].y, off)));
+    if constexpr (NT > 32) {
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+            for (int q = 0; q < ROWS; ++q) box[q][threadIdx.x >> 5] = v[q];
         __syncthreads();
-        v = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < NT / 32; ++i) v.x += box[i].x, v.y += box[i].y;
-    }
-    return v;
-}
-template <int NT>
-__device__ __forceinline__ float2 row_sum_max(float2 v, float2 *box) {   // x summed, y's maximum
+        for (int q = 0; q < ROWS; ++q) {
+            v[q] = box[q][0];
 #pragma unroll
-    for (int off = (NT < 32 ? NT : 32) / 2; off > 0; off >>= 1) {
-        v.x += __shfl_xor_sync(~0u, v.x, off);
-        v.y = fmaxf(v.y, __shfl_xor_sync(~0u, v.y, off));
+            for (int i = 1; i < NT / 32; ++i) v[q] = join(v[q], box[q][i]);
+        }
     }
-    if (NT > 32) {
-        if ((threadIdx.x & 31) == 0) box[threadIdx.x >> 5] = v;
-        __syncthreads();
-        v = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int i = 0; i < NT / 32; ++i) v.x += box[i].x, v.y = fmaxf(v.y, box[i].y);
-    }
-    return v;
 }
 
 // Scale of a group whose largest |y| is `top`: 1 for zeros, and never so small that its
@@ -123,101 +120,115 @@ __device__ __forceinline__ void store_fp8(unsigned char *p, const float (&y)[V],
     }
 }
 
-// V values a vector, K vectors a thread, NT threads a row, ROWS rows in flight a thread.
-// GROUPS: 8-bit output with a scale for each p.group columns (128: 16 neighbouring lanes);
-// otherwise with FP8 a scale a row.
-template <typename IO, int V, int K, int NT, int ROWS, bool RES, bool FP8, bool GROUPS>
+// Vector (row i, column c) of a tensor, zeros where it is none: the address is chosen, not the
+// load, so that no branch stands between the loads.
+template <typename IO, int V>
+__device__ __forceinline__ Pack<IO, V> row_pack(const void *base, long long at, bool ok) {
+    Pack<IO, V> x = load_pack<IO, V>(static_cast<const IO *>(base) + (ok ? at : 0));
+    if (!ok) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) x.v[j] = from_f32<IO>(0.f);
+    }
+    return x;
+}
+
+// V values a vector, K vectors a thread, NT threads a row, ROWS rows a thread at a time (their
+// loads in flight together, one reduction for all of them).  FP8: 1 a scale a row, 2 a scale for
+// each 128 columns (16 neighbouring lanes).
+template <typename IO, int V, int K, int NT, int ROWS, bool RES, int FP8>
 __global__ void __launch_bounds__(NT < 256 ? 256 : NT) norm_kernel(const NormParams p) {
     constexpr int kBlock = NT < 256 ? 256 : NT;
     constexpr int kRowsBlock = NT <= 32 ? kBlock / NT : 1;
     static_assert(NT <= 32 || NT == kBlock, "a row has part of a warp, a warp or a CTA");
     using X = Pack<IO, V>;
-    __shared__ float2 box[2][NT > 32 ? NT / 32 : 1];
+    using W = Pack<float, V>;
+    __shared__ float2 box[2][ROWS][NT > 32 ? NT / 32 : 1];
     const int t = threadIdx.x % NT;
     const long long stride = (long long)gridDim.x * kRowsBlock * ROWS;
     const int C = p.C;
     int turn = 0;
-    // the loop runs by whole blocks: threads without a row take part in the shuffles
+    // the loop runs by whole blocks: threads without a row take part in the reductions
+#pragma unroll 1
     for (long long base = (long long)blockIdx.x * kRowsBlock * ROWS; base < p.rows; base += stride) {
+        const long long i0 = base + threadIdx.x / NT;   // row q is i0 + q kRowsBlock
         X x[ROWS][K], r[RES ? ROWS : 1][RES ? K : 1];
 #pragma unroll
-        for (int q = 0; q < ROWS; ++q) {
-            const long long i = base + q * kRowsBlock + threadIdx.x / NT;
+        for (int q = 0; q < ROWS; ++q)
 #pragma unroll
             for (int k = 0; k < K; ++k) {
+                const long long i = i0 + q * kRowsBlock;
                 const int c = (k * NT + t) * V;
-                if (i < p.rows && c < C) {
-                    x[q][k] = load_pack<IO, V>(static_cast<const IO *>(p.x) + i * C + c);
-                    if (RES) r[RES ? q : 0][RES ? k : 0] = load_pack<IO, V>(static_cast<const IO *>(p.residual) + i * C + c);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        x[q][k].v[j] = from_f32<IO>(0.f);
-                        if (RES) r[RES ? q : 0][RES ? k : 0].v[j] = from_f32<IO>(0.f);
-                    }
-                }
+                const bool ok = i < p.rows && c < C;
+                x[q][k] = row_pack<IO, V>(p.x, i * C + c, ok);
+                if constexpr (RES) r[q][k] = row_pack<IO, V>(p.residual, i * C + c, ok);
             }
-        }
+        float2 sum[ROWS];
 #pragma unroll
-        for (int q = 0; q < ROWS; ++q) {
-            const long long i = base + q * kRowsBlock + threadIdx.x / NT;
-            const bool live = i < p.rows;
-            float2 sum = make_float2(0.f, 0.f);
+        for (int q = 0; q < ROWS; ++q) sum[q] = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const int c = (k * NT + t) * V;
-                if (RES) {
+        for (int k = 0; k < K; ++k) {
+            const int c = (k * NT + t) * V;
+            W w;
+            if (FP8 == 1) w = load_pack<float, V>(p.w + (c < C ? c : 0));
 #pragma unroll
-                    for (int j = 0; j < V; ++j)
-                        x[q][k].v[j] = from_f32<IO>(to_f32(x[q][k].v[j]) + to_f32(r[RES ? q : 0][RES ? k : 0].v[j]));
-                    if (live && c < C) store_pack<IO, V>(static_cast<IO *>(p.h) + i * C + c, x[q][k]);
+            for (int q = 0; q < ROWS; ++q) {
+                const long long i = i0 + q * kRowsBlock;
+                if constexpr (RES) {
+#pragma unroll
+                    for (int j = 0; j < V; ++j) x[q][k].v[j] = from_f32<IO>(to_f32(x[q][k].v[j]) + to_f32(r[q][k].v[j]));
+                    if (i < p.rows && c < C) store_pack<IO, V>(static_cast<IO *>(p.h) + i * C + c, x[q][k]);
                 }
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     const float f = to_f32(x[q][k].v[j]);
-                    sum.x = fmaf(f, f, sum.x);
-                    if (FP8 && !GROUPS && c < C) sum.y = fmaxf(sum.y, fabsf(f * p.w[c + j]));
+                    sum[q].x = fmaf(f, f, sum[q].x);
+                    if (FP8 == 1) sum[q].y = fmaxf(sum[q].y, fabsf(f * w.v[j]));   // rows without c hold 0
                 }
             }
-            sum = FP8 && !GROUPS ? row_sum_max<NT>(sum, box[turn]) : row_sum<NT>(sum, box[turn]);
-            turn ^= 1;
-            const float rstd = rsqrtf(fmaf(sum.x, p.inv_c, p.eps));
-            const long long o = out_row(live ? i : 0, p.H, p.T) * C;
-            float inv = 1.f;
-            if (FP8 && !GROUPS) {
-                const float scale = fp8_scale(sum.y * rstd);
-                inv = 1.f / scale;
-                if (live && t == 0) p.scales[o / C] = scale;
-            }
+        }
+        row_sums<NT, ROWS, FP8 == 1>(sum, box[turn]);
+        turn ^= 1;
+        float rstd[ROWS], inv[ROWS];
+        long long o[ROWS];
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const int c = (k * NT + t) * V;
+        for (int q = 0; q < ROWS; ++q) {
+            const long long i = i0 + q * kRowsBlock;
+            rstd[q] = rsqrtf(fmaf(sum[q].x, p.inv_c, p.eps));
+            const long long row = out_row(p, i < p.rows ? i : 0);
+            o[q] = row * C;
+            if (FP8 == 1) {
+                const float scale = fp8_scale(sum[q].y * rstd[q]);
+                inv[q] = 1.f / scale;
+                if (i < p.rows && t == 0) p.scales[row] = scale;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = (k * NT + t) * V;
+            const W w = load_pack<float, V>(p.w + (c < C ? c : 0));
+#pragma unroll
+            for (int q = 0; q < ROWS; ++q) {
+                const bool ok = i0 + q * kRowsBlock < p.rows && c < C;
                 float y[V];
-                float top = 0.f;
-                if (c < C) {
-                    const Pack<float, V> w = load_pack<float, V>(p.w + c);
 #pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        y[j] = to_f32(x[q][k].v[j]) * rstd * w.v[j];
-                        top = fmaxf(top, fabsf(y[j]));
-                    }
-                }
-                if (FP8 && GROUPS) {
+                for (int j = 0; j < V; ++j) y[j] = to_f32(x[q][k].v[j]) * rstd[q] * w.v[j];
+                if constexpr (FP8 == 2) {
+                    float top = 0.f;
+#pragma unroll
+                    for (int j = 0; j < V; ++j) top = fmaxf(top, fabsf(y[j]));
 #pragma unroll
                     for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, off));
                     const float scale = fp8_scale(top);
-                    inv = 1.f / scale;
-                    if (live && c < C && (threadIdx.x & 15) == 0) p.scales[(o + c) / 128] = scale;
+                    inv[q] = 1.f / scale;
+                    if (ok && (threadIdx.x & 15) == 0) p.scales[(o[q] + c) / 128] = scale;
                 }
-                if (live && c < C) {
-                    if constexpr (FP8) {
-                        store_fp8<V>(static_cast<unsigned char *>(p.y) + o + c, y, inv);
-                    } else {
-                        X out;
+                if constexpr (FP8) {
+                    if (ok) store_fp8<V>(static_cast<unsigned char *>(p.y) + o[q] + c, y, inv[q]);
+                } else {
+                    X out;
 #pragma unroll
-                        for (int j = 0; j < V; ++j) out.v[j] = from_f32<IO>(y[j]);
-                        store_pack<IO, V>(static_cast<IO *>(p.y) + o + c, out);
-                    }
+                    for (int j = 0; j < V; ++j) out.v[j] = from_f32<IO>(y[j]);
+                    if (ok) store_pack<IO, V>(static_cast<IO *>(p.y) + o[q] + c, out);
                 }
             }
         }
@@ -230,7 +241,8 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT) norm_backward_kernel(cons
     constexpr int kRowsBlock = NT <= 32 ? kBlock / NT : 1;
     static_assert(NT <= 32 || NT == kBlock, "a row has part of a warp, a warp or a CTA");
     using X = Pack<IO, V>;
-    __shared__ float2 box[2][NT > 32 ? NT / 32 : 1];
+    using W = Pack<float, V>;
+    __shared__ float2 box[2][ROWS][NT > 32 ? NT / 32 : 1];
     __shared__ float fold[NT <= 32 ? kBlock * K * V : 1];
     const int t = threadIdx.x % NT;
     const long long stride = (long long)gridDim.x * kRowsBlock * ROWS;
@@ -241,62 +253,61 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT) norm_backward_kernel(cons
 #pragma unroll
         for (int j = 0; j < V; ++j) dw[k][j] = 0.f;
     int turn = 0;
+#pragma unroll 1
     for (long long base = (long long)blockIdx.x * kRowsBlock * ROWS; base < p.rows; base += stride) {
+        const long long i0 = base + threadIdx.x / NT;
         X x[ROWS][K], g[ROWS][K], r[DRES ? ROWS : 1][DRES ? K : 1];
 #pragma unroll
         for (int q = 0; q < ROWS; ++q) {
-            const long long i = base + q * kRowsBlock + threadIdx.x / NT;
-            const long long o = i < p.rows ? out_row(i, p.H, p.T) * C : 0;
+            const long long i = i0 + q * kRowsBlock;
+            const long long o = out_row(p, i < p.rows ? i : 0) * C;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 const int c = (k * NT + t) * V;
-                if (i < p.rows && c < C) {
-                    x[q][k] = load_pack<IO, V>(static_cast<const IO *>(p.h) + i * C + c);
-                    g[q][k] = load_pack<IO, V>(static_cast<const IO *>(p.dy) + o + c);
-                    if (DRES) r[DRES ? q : 0][DRES ? k : 0] = load_pack<IO, V>(static_cast<const IO *>(p.dres) + i * C + c);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < V; ++j) x[q][k].v[j] = g[q][k].v[j] = from_f32<IO>(0.f);
-                }
+                const bool ok = i < p.rows && c < C;
+                x[q][k] = row_pack<IO, V>(p.h, i * C + c, ok);
+                g[q][k] = row_pack<IO, V>(p.dy, o + c, ok);
+                if constexpr (DRES) r[q][k] = row_pack<IO, V>(p.dres, i * C + c, ok);
             }
         }
+        float2 sum[ROWS];
 #pragma unroll
-        for (int q = 0; q < ROWS; ++q) {
-            const long long i = base + q * kRowsBlock + threadIdx.x / NT;
-            float2 sum = make_float2(0.f, 0.f);
+        for (int q = 0; q < ROWS; ++q) sum[q] = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const int c = (k * NT + t) * V;
-                if (c < C) {
-                    const Pack<float, V> w = load_pack<float, V>(p.w + c);
+        for (int k = 0; k < K; ++k) {
+            const int c = (k * NT + t) * V;
+            const W w = load_pack<float, V>(p.w + (c < C ? c : 0));
 #pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        const float f = to_f32(x[q][k].v[j]);
-                        sum.x = fmaf(f, f, sum.x);
-                        sum.y = fmaf(to_f32(g[q][k].v[j]) * w.v[j], f, sum.y);
-                    }
+            for (int q = 0; q < ROWS; ++q)
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float f = to_f32(x[q][k].v[j]);
+                    sum[q].x = fmaf(f, f, sum[q].x);
+                    sum[q].y = fmaf(to_f32(g[q][k].v[j]) * w.v[j], f, sum[q].y);
                 }
-            }
-            sum = row_sum<NT>(sum, box[turn]);
-            turn ^= 1;
-            const float rstd = rsqrtf(fmaf(sum.x, p.inv_c, p.eps));
-            const float mean = sum.y * rstd * p.inv_c;   // mean(p n)
+        }
+        row_sums<NT, ROWS, false>(sum, box[turn]);
+        turn ^= 1;
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const int c = (k * NT + t) * V;
-                if (i < p.rows && c < C) {
-                    const Pack<float, V> w = load_pack<float, V>(p.w + c);
-                    X out;
+        for (int k = 0; k < K; ++k) {
+            const int c = (k * NT + t) * V;
+            const W w = load_pack<float, V>(p.w + (c < C ? c : 0));
 #pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        const float n = to_f32(x[q][k].v[j]) * rstd, d = to_f32(g[q][k].v[j]);
-                        dw[k][j] = fmaf(d, n, dw[k][j]);
-                        float v = rstd * (d * w.v[j] - n * mean);
-                        if (DRES) v += to_f32(r[DRES ? q : 0][DRES ? k : 0].v[j]);
-                        out.v[j] = from_f32<IO>(v);
-                    }
-                    store_pack<IO, V>(static_cast<IO *>(p.dx) + i * C + c, out);
+            for (int q = 0; q < ROWS; ++q) {
+                const long long i = i0 + q * kRowsBlock;
+                const float rstd = i < p.rows ? rsqrtf(fmaf(sum[q].x, p.inv_c, p.eps)) : 0.f;
+                const float mean = sum[q].y * rstd * p.inv_c;   // mean(p n)
+                X out;
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    // a row or a column that is none holds zeros and adds none to dw
+                    const float n = to_f32(x[q][k].v[j]) * rstd, d = to_f32(g[q][k].v[j]);
+                    dw[k][j] = fmaf(d, n, dw[k][j]);
+                    float v = rstd * (d * w.v[j] - n * mean);
+                    if constexpr (DRES) v += to_f32(r[q][k].v[j]);
+                    out.v[j] = from_f32<IO>(v);
                 }
+                if (i < p.rows && c < C) store_pack<IO, V>(static_cast<IO *>(p.dx) + i * C + c, out);
             }
         }
     }
@@ -346,31 +357,42 @@ __global__ void __launch_bounds__(256) norm_weight_kernel(int blocks, int C, con
 
 // ------------------------------------------------------------------------------- host side
 
-// Blocks for `rows` rows: all at once up to what the SMs hold, then in a loop.
-template <typename F>
-unsigned loop_blocks(F kernel, int threads, long long rows, int rows_block) {
-    int per_sm = 1;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, 0) != cudaSuccess) {
-        (void)cudaGetLastError();
-        per_sm = 1;
+// Blocks for `rows` rows: all at once up to what the SMs hold (asked once a process; the same on
+// every B200), then in a loop.
+template <auto KERNEL>
+unsigned loop_blocks(int threads, long long rows, int rows_block) {
+    static std::atomic<int> known{0};
+    int per_sm = known.load(std::memory_order_relaxed);
+    if (per_sm == 0) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, KERNEL, threads, 0) != cudaSuccess || per_sm < 1) {
+            (void)cudaGetLastError();
+            per_sm = 1;
+        }
+        known.store(per_sm, std::memory_order_relaxed);
     }
-    const long long need = (rows + rows_block - 1) / rows_block, most = 148ll * (per_sm < 1 ? 1 : per_sm);
+    const long long need = (rows + rows_block - 1) / rows_block, most = 148ll * per_sm;
     return (unsigned)(need < most ? need : most);
 }
 
-template <typename IO, int V, int K, int NT, int ROWS, bool RES, bool FP8, bool GROUPS>
+template <typename P, typename A>
+void fill_rows(P &p, const A &a) {
+    p.rows = (long long)a.B * a.H * a.T;
+    p.H = a.H; p.T = a.T; p.C = a.C;
+    p.byT = FastDiv(a.T);
+    p.byH = FastDiv(a.H);
+    p.eps = a.eps;
+    p.inv_c = 1.f / (float)a.C;
+}
+
+template <typename IO, int V, int K, int NT, int ROWS, bool RES, int FP8>
 cudaError_t launch_forward(const NormArgs &a) {
     constexpr int kBlock = NT < 256 ? 256 : NT, kRowsBlock = NT <= 32 ? kBlock / NT : 1;
     NormParams p;
     p.x = a.x; p.residual = a.residual; p.w = a.w;
     p.h = a.h; p.y = a.y; p.scales = a.scales;
-    p.rows = (long long)a.B * a.H * a.T;
-    p.H = a.H; p.T = a.T; p.C = a.C;
-    p.group = a.group;
-    p.eps = a.eps;
-    p.inv_c = 1.f / (float)a.C;
-    auto kernel = norm_kernel<IO, V, K, NT, ROWS, RES, FP8, GROUPS>;
-    const unsigned blocks = loop_blocks(kernel, kBlock, p.rows, kRowsBlock * ROWS);
+    fill_rows(p, a);
+    constexpr auto kernel = norm_kernel<IO, V, K, NT, ROWS, RES, FP8>;
+    const unsigned blocks = loop_blocks<kernel>(kBlock, p.rows, kRowsBlock * ROWS);
     timer_begin(a.stream);
     kernel<<<blocks, kBlock, 0, a.stream>>>(p);
     timer_end(a.stream);
@@ -380,17 +402,13 @@ cudaError_t launch_forward(const NormArgs &a) {
 
 template <typename IO, int V, int K, int NT, int ROWS>
 cudaError_t forward_kind(const NormArgs &a) {
-    if (!a.fp8) {
-        return a.residual ? launch_forward<IO, V, K, NT, ROWS, true, false, false>(a)
-                          : launch_forward<IO, V, K, NT, ROWS, false, false, false>(a);
-    }
+    if (!a.fp8)
+        return a.residual ? launch_forward<IO, V, K, NT, ROWS, true, 0>(a) : launch_forward<IO, V, K, NT, ROWS, false, 0>(a);
     if constexpr (V == 8 && NT >= 16) {
         if (a.group == 128)
-            return a.residual ? launch_forward<IO, V, K, NT, ROWS, true, true, true>(a)
-                              : launch_forward<IO, V, K, NT, ROWS, false, true, true>(a);
+            return a.residual ? launch_forward<IO, V, K, NT, ROWS, true, 2>(a) : launch_forward<IO, V, K, NT, ROWS, false, 2>(a);
     }
-    return a.residual ? launch_forward<IO, V, K, NT, ROWS, true, true, false>(a)
-                      : launch_forward<IO, V, K, NT, ROWS, false, true, false>(a);
+    return a.residual ? launch_forward<IO, V, K, NT, ROWS, true, 1>(a) : launch_forward<IO, V, K, NT, ROWS, false, 1>(a);
 }
 
 template <typename IO>
@@ -399,15 +417,17 @@ cudaError_t forward_io(const NormArgs &a) {
     if (C % 8) {
         if (C <= 256) return forward_kind<IO, 1, 8, 32, 1>(a);
         if (C <= 2048) return forward_kind<IO, 1, 8, 256, 1>(a);
+        if (C <= 8192) return forward_kind<IO, 1, 8, 1024, 1>(a);
         return forward_kind<IO, 1, 16, 1024, 1>(a);
     }
-    if (C <= 64) return forward_kind<IO, 8, 1, 8, 4>(a);
-    if (C <= 128) return forward_kind<IO, 8, 1, 16, 4>(a);
-    if (C <= 256) return forward_kind<IO, 8, 1, 32, 4>(a);
-    if (C <= 512) return forward_kind<IO, 8, 2, 32, 2>(a);
+    constexpr int M = sizeof(IO) == 2 ? 2 : 1;   // rows at a time by the registers they take
+    if (C <= 64) return forward_kind<IO, 8, 1, 8, 2 * M>(a);
+    if (C <= 128) return forward_kind<IO, 8, 1, 16, 2 * M>(a);
+    if (C <= 256) return forward_kind<IO, 8, 1, 32, 2 * M>(a);
+    if (C <= 512) return forward_kind<IO, 8, 2, 32, M>(a);
     if (C <= 1024) return forward_kind<IO, 8, 4, 32, 1>(a);
-    if (C <= 2048) return forward_kind<IO, 8, 1, 256, 1>(a);
-    if (C <= 4096) return forward_kind<IO, 8, 2, 256, 1>(a);
+    if (C <= 2048) return forward_kind<IO, 8, 1, 256, 2 * M>(a);
+    if (C <= 4096) return forward_kind<IO, 8, 2, 256, M>(a);
     if (C <= 8192) return forward_kind<IO, 8, 4, 256, 1>(a);
     return forward_kind<IO, 8, 4, 512, 1>(a);
 }
@@ -418,12 +438,9 @@ cudaError_t launch_backward(const NormBackwardArgs &a) {
     NormBackwardParams p;
     p.h = a.h; p.dy = a.dy; p.dres = a.dres; p.w = a.w;
     p.dx = a.dx; p.partial = a.partial;
-    p.rows = (long long)a.B * a.H * a.T;
-    p.H = a.H; p.T = a.T; p.C = a.C;
-    p.eps = a.eps;
-    p.inv_c = 1.f / (float)a.C;
-    auto kernel = norm_backward_kernel<IO, V, K, NT, ROWS, DRES>;
-    unsigned blocks = loop_blocks(kernel, kBlock, p.rows, kRowsBlock * ROWS);
+    fill_rows(p, a);
+    constexpr auto kernel = norm_backward_kernel<IO, V, K, NT, ROWS, DRES>;
+    unsigned blocks = loop_blocks<kernel>(kBlock, p.rows, kRowsBlock * ROWS);
     if (blocks > (unsigned)kMaxPartials) blocks = kMaxPartials;
     timer_begin(a.stream);
     kernel<<<blocks, kBlock, 0, a.stream>>>(p);
@@ -449,15 +466,17 @@ cudaError_t backward_io(const NormBackwardArgs &a) {
     if (C % 8) {
         if (C <= 256) return backward_kind<IO, 1, 8, 32, 1>(a);
         if (C <= 2048) return backward_kind<IO, 1, 8, 256, 1>(a);
+        if (C <= 8192) return backward_kind<IO, 1, 8, 1024, 1>(a);
         return backward_kind<IO, 1, 16, 1024, 1>(a);
     }
-    if (C <= 64) return backward_kind<IO, 8, 1, 8, 2>(a);
-    if (C <= 128) return backward_kind<IO, 8, 1, 16, 2>(a);
-    if (C <= 256) return backward_kind<IO, 8, 1, 32, 2>(a);
+    constexpr int M = sizeof(IO) == 2 ? 2 : 1;
+    if (C <= 64) return backward_kind<IO, 8, 1, 8, M>(a);
+    if (C <= 128) return backward_kind<IO, 8, 1, 16, M>(a);
+    if (C <= 256) return backward_kind<IO, 8, 1, 32, M>(a);
     if (C <= 512) return backward_kind<IO, 8, 2, 32, 1>(a);
-    if (C <= 2048) return backward_kind<IO, 8, 1, 256, 1>(a);
-    if (C <= 4096) return backward_kind<IO, 8, 1, 512, 1>(a);
-    if (C <= 8192) return backward_kind<IO, 8, 1, 1024, 1>(a);
+    if (C <= 2048) return backward_kind<IO, 8, 1, 256, 2 * M>(a);
+    if (C <= 4096) return backward_kind<IO, 8, 2, 256, M>(a);
+    if (C <= 8192) return backward_kind<IO, 8, 2, 512, 1>(a);
     return backward_kind<IO, 8, 2, 1024, 1>(a);
 }
 

@@ -23,11 +23,13 @@
 #include "la_internal.cuh"
 #include "vec.cuh"
 
+#include <type_traits>
+
 namespace la {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;   // heads in flight
+constexpr int MINB = 3;
 
 struct RotaryParams {
     const void *x[2];      // q, k
@@ -61,24 +63,26 @@ __device__ __forceinline__ long long row_of(bool token_major, long long b, long 
 
 // PAIRS pairs a thread: 8 (rows in 16-byte vectors; r a multiple of 16, d of 8), or 1.
 // Units behind the rotated ones copy 2 * PAIRS values (none when in place).
-template <typename IO, int PAIRS, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryParams p) {
+// SHARE: the HS = SHARE threads that hold the same pairs of one token are lanes of one warp,
+// units apart: each forms PAIRS / SHARE of the angles and the others get them by shuffles.
+template <typename IO, int PAIRS, bool INTERLEAVED, int SHARE>
+__global__ void __launch_bounds__(kThreads, PAIRS == 1 ? 4 : MINB) rotary_kernel(const RotaryParams p) {
     using X = Pack<IO, PAIRS>;
     const long long idx = (long long)blockIdx.x * kThreads + threadIdx.x;
-    long long rest;
+    long long token;
     int u, hs;
     if (p.tokens * p.units * p.HS <= UINT32_MAX) {
         const unsigned i = (unsigned)idx;
         u = i % (unsigned)p.units;
         hs = i / (unsigned)p.units % (unsigned)p.HS;
-        rest = i / (unsigned)p.units / (unsigned)p.HS;
+        token = i / (unsigned)p.units / (unsigned)p.HS;
     } else {
         u = (int)(idx % p.units);
         hs = (int)(idx / p.units % p.HS);
-        rest = idx / p.units / p.HS;
+        token = idx / p.units / p.HS;
     }
-    if (rest >= p.tokens) return;
-    const long long b = rest / p.T, t = rest - b * p.T;
+    if (token >= p.tokens) return;   // with SHARE: a token's threads go or stay together
+    const long long b = token / p.T, t = token - b * p.T;
     const int turned = p.r / (2 * PAIRS);
     const bool turn = u < turned;
     // the two vectors of the thread in a head row
@@ -92,53 +96,74 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryParams p) 
     }
     const bool second = e1 < p.d;   // false: the last copied vector of a row stands alone
     float cs[PAIRS], sn[PAIRS];
-    if (turn) {
-        const double pos = (double)(p.positions ? (long long)p.positions[rest] : p.start + t);
+    const double pos = (double)(p.positions ? (long long)p.positions[token] : p.start + t);
+    if constexpr (SHARE > 1) {
+        constexpr int kOwn = PAIRS / SHARE;
+        float c[kOwn], s[kOwn];
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j)
+            if (turn) angle(pos, p.freqs[u * PAIRS + hs * kOwn + j], s[j], c[j]);
+        const unsigned here = __activemask();
+        const int lane = threadIdx.x & 31, first = lane - hs * p.units;   // the lane of hs = 0
 #pragma unroll
         for (int j = 0; j < PAIRS; ++j) {
-            angle(pos, p.freqs[u * PAIRS + j], sn[j], cs[j]);
-            cs[j] *= p.scale;
-            sn[j] *= p.scale * p.sign;
+            cs[j] = __shfl_sync(here, c[j % kOwn], first + j / kOwn * p.units);
+            sn[j] = __shfl_sync(here, s[j % kOwn], first + j / kOwn * p.units);
         }
+    } else if (turn) {
+#pragma unroll
+        for (int j = 0; j < PAIRS; ++j) angle(pos, p.freqs[u * PAIRS + j], sn[j], cs[j]);
     }
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        const int H = p.heads[which];
-        if (H == 0) continue;
-        long long xh, yh;
-        const IO *x = static_cast<const IO *>(p.x[which]) + row_of(p.x_tokens, b, t, p.T, H, p.d, xh);
-        IO *y = static_cast<IO *>(p.y[which]) + row_of(p.y_tokens, b, t, p.T, H, p.d, yh);
-        for (int h0 = hs; h0 < H; h0 += kUnroll * p.HS) {
-            X v0[kUnroll], v1[kUnroll];
+    for (int j = 0; j < PAIRS; ++j) {
+        cs[j] *= p.scale;
+        sn[j] *= p.scale * p.sign;
+    }
+    auto rotate = [&](X &v0, X &v1) {
 #pragma unroll
-            for (int i = 0; i < kUnroll; ++i) {
-                const int h = h0 + i * p.HS;
-                if (h < H) {
-                    v0[i] = load_pack<IO, PAIRS>(x + h * xh + e0);
-                    if (second) v1[i] = load_pack<IO, PAIRS>(x + h * xh + e1);
-                }
+        for (int j = 0; j < PAIRS; ++j) {
+            // interleaved pairs lie next to each other across the two vectors
+            IO &a = INTERLEAVED ? (2 * j < PAIRS ? v0.v[(2 * j) % PAIRS] : v1.v[(2 * j) % PAIRS]) : v0.v[j];
+            IO &c = INTERLEAVED ? (2 * j + 1 < PAIRS ? v0.v[(2 * j + 1) % PAIRS] : v1.v[(2 * j + 1) % PAIRS]) : v1.v[j];
+            const float fa = to_f32(a), fc = to_f32(c);
+            a = from_f32<IO>(fa * cs[j] - fc * sn[j]);
+            c = from_f32<IO>(fa * sn[j] + fc * cs[j]);
+        }
+    };
+    const int off = second ? e1 - e0 : 0;   // a lone vector is handled twice
+#pragma unroll 1
+    for (int w = 0; w < 2; ++w) {
+        long long xs, ys;
+        const IO *x = static_cast<const IO *>(w ? p.x[1] : p.x[0]);
+        IO *y = static_cast<IO *>(w ? p.y[1] : p.y[0]);
+        const int H = w ? p.heads[1] : p.heads[0];
+        x += row_of(p.x_tokens, b, t, p.T, H, p.d, xs) + e0;
+        y += row_of(p.y_tokens, b, t, p.T, H, p.d, ys) + e0;
+        x += hs * xs;
+        y += hs * ys;
+        xs *= p.HS;
+        ys *= p.HS;
+        int n = hs < H ? (H - hs + p.HS - 1) / p.HS : 0;   // the thread's heads, two at a time
+#pragma unroll 1
+        for (; n > 1; n -= 2) {
+            X a0 = load_pack<IO, PAIRS>(x), a1 = load_pack<IO, PAIRS>(x + off);
+            X b0 = load_pack<IO, PAIRS>(x + xs), b1 = load_pack<IO, PAIRS>(x + xs + off);
+            if (turn) {
+                rotate(a0, a1);
+                rotate(b0, b1);
             }
-#pragma unroll
-            for (int i = 0; i < kUnroll; ++i) {
-                const int h = h0 + i * p.HS;
-                if (h >= H) break;
-                if (turn) {
-#pragma unroll
-                    for (int j = 0; j < PAIRS; ++j) {
-                        // interleaved pairs lie next to each other across the two vectors
-                        IO &a = INTERLEAVED ? (2 * j < PAIRS ? v0[i].v[(2 * j) % PAIRS] : v1[i].v[(2 * j) % PAIRS])
-                                            : v0[i].v[j];
-                        IO &c = INTERLEAVED ? (2 * j + 1 < PAIRS ? v0[i].v[(2 * j + 1) % PAIRS]
-                                                                 : v1[i].v[(2 * j + 1) % PAIRS])
-                                            : v1[i].v[j];
-                        const float fa = to_f32(a), fc = to_f32(c);
-                        a = from_f32<IO>(fa * cs[j] - fc * sn[j]);
-                        c = from_f32<IO>(fa * sn[j] + fc * cs[j]);
-                    }
-                }
-                store_pack<IO, PAIRS>(y + h * yh + e0, v0[i]);
-                if (second) store_pack<IO, PAIRS>(y + h * yh + e1, v1[i]);
-            }
+            store_pack<IO, PAIRS>(y, a0);
+            store_pack<IO, PAIRS>(y + off, a1);
+            store_pack<IO, PAIRS>(y + ys, b0);
+            store_pack<IO, PAIRS>(y + ys + off, b1);
+            x += 2 * xs;
+            y += 2 * ys;
+        }
+        if (n) {
+            X a0 = load_pack<IO, PAIRS>(x), a1 = load_pack<IO, PAIRS>(x + off);
+            if (turn) rotate(a0, a1);
+            store_pack<IO, PAIRS>(y, a0);
+            store_pack<IO, PAIRS>(y + off, a1);
         }
     }
 }
@@ -162,16 +187,30 @@ cudaError_t launch_pairs(const RotaryArgs &a) {
     p.y_tokens = a.y_tokens;
     const bool in_place = a.yq == a.q && (a.Hk == 0 || a.yk == a.k);
     p.units = a.r / (2 * PAIRS) + (in_place ? 0 : (a.d - a.r + 2 * PAIRS - 1) / (2 * PAIRS));
-    // Four threads a token share its heads; more of them where the tokens alone would leave the
-    // SMs with less than a few warps each (decoding).
-    const int most = a.Hq > a.Hk ? a.Hq : a.Hk;
-    p.HS = most < 4 ? most : 4;
-    while (p.HS < most && p.tokens * p.units * p.HS < 148ll * 512) p.HS = 2 * p.HS < most ? 2 * p.HS : most;
+    // Four threads a token share its heads (eight where the units of a row are four, so that they
+    // fill a warp); more of them where the tokens alone would leave the SMs with less than a few
+    // warps each (decoding).
+    const int heads = a.Hq + a.Hk;
+    const int usual = p.units == 4 ? 8 : 4;
+    p.HS = heads < usual ? heads : usual;
+    while (p.HS < heads && p.tokens * p.units * p.HS < 148ll * 512) p.HS = 2 * p.HS < heads ? 2 * p.HS : heads;
+    const bool share = PAIRS == 8 && p.units * p.HS == 32 && (p.HS == 4 || p.HS == 8);
     const long long blocks = (p.tokens * p.units * p.HS + kThreads - 1) / kThreads;
     if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
     timer_begin(a.stream);
-    if (a.interleaved) rotary_kernel<IO, PAIRS, true><<<(unsigned)blocks, kThreads, 0, a.stream>>>(p);
-    else rotary_kernel<IO, PAIRS, false><<<(unsigned)blocks, kThreads, 0, a.stream>>>(p);
+    auto go = [&](auto turn_next, auto share_by) {
+        rotary_kernel<IO, PAIRS, decltype(turn_next)::value, decltype(share_by)::value>
+            <<<(unsigned)blocks, kThreads, 0, a.stream>>>(p);
+    };
+    auto pick = [&](auto turn_next) {
+        if constexpr (PAIRS == 8) {
+            if (share && p.HS == 4) return go(turn_next, std::integral_constant<int, 4>{});
+            if (share) return go(turn_next, std::integral_constant<int, 8>{});
+        }
+        go(turn_next, std::integral_constant<int, 1>{});
+    };
+    if (a.interleaved) pick(std::true_type{});
+    else pick(std::false_type{});
     timer_end(a.stream);
     note_launches(1);
     return cudaGetLastError();

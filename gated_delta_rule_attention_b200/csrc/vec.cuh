@@ -21,4 +21,17 @@ __device__ __forceinline__ void store_pack(T *p, const Pack<T, V> &x) {
     *reinterpret_cast<Pack<T, V> *>(p) = x;
 }
 
+// n / d for 0 <= n < 2^31 by a product: with s = ceil(log2 d) and m = floor(2^32 (2^s - d) / d) + 1,
+// n / d = (hi32(n m) + n) >> s (Granlund and Montgomery, "Division by invariant integers using
+// multiplication", 1994; the sum stays below 2^32 for these n).
+struct FastDiv {
+    unsigned d = 1, m = 1, s = 0;
+    FastDiv() = default;
+    explicit FastDiv(unsigned by) : d(by) {
+        while (s < 31 && (1u << s) < d) ++s;
+        m = (unsigned)(((1ull << 32) * ((1ull << s) - d)) / d + 1);
+    }
+    __device__ __forceinline__ unsigned operator()(unsigned n) const { return (__umulhi(n, m) + n) >> s; }
+};
+
 }  // namespace la
