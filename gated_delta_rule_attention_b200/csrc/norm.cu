@@ -21,7 +21,7 @@
 // two sums go through the threads of the row (shuffles within a warp or a part of one, shared
 // memory for a row of a whole CTA), and it is written once.  Threads of a row: C / 8 up to a
 // warp, then up to eight vectors a lane, then a CTA a row; rows are taken in a loop, so the
-// weights stay in L1.  dw: every thread keeps its columns' sums over its CTA's rows in
+// weights stay in registers or L1.  dw: every thread keeps its columns' sums over its CTA's rows in
 // registers, each CTA writes one row of partial sums, and a second kernel adds those in a fixed
 // order.
 #include "la_internal.cuh"
@@ -34,7 +34,7 @@ namespace la {
 namespace {
 
 constexpr float kFp8Max = 448.f;   // largest e4m3 value
-constexpr int kMaxPartials = 148 * 4;
+constexpr int kMaxPartials = 148 * 8;   // CTAs of the backward pass
 
 struct NormParams {
     const void *x, *residual;
@@ -136,8 +136,8 @@ __device__ __forceinline__ Pack<IO, V> row_pack(const void *base, long long at, 
 // loads in flight together, one reduction for all of them).  FP8: 1 a scale a row, 2 a scale for
 // each 128 columns (16 neighbouring lanes).
 template <typename IO, int V, int K, int NT, int ROWS, bool RES, int FP8>
-__global__ void __launch_bounds__(NT < 256 ? 256 : NT) norm_kernel(const NormParams p) {
-    constexpr int kBlock = NT < 256 ? 256 : NT;
+__global__ void __launch_bounds__(NT <= 32 ? 256 : NT, (RES && ROWS * K * V >= 32 ? 768 : 1024) / (NT <= 32 ? 256 : NT)) norm_kernel(const NormParams p) {
+    constexpr int kBlock = NT <= 32 ? 256 : NT;
     constexpr int kRowsBlock = NT <= 32 ? kBlock / NT : 1;
     static_assert(NT <= 32 || NT == kBlock, "a row has part of a warp, a warp or a CTA");
     using X = Pack<IO, V>;
@@ -146,6 +146,15 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT) norm_kernel(const NormPar
     const int t = threadIdx.x % NT;
     const long long stride = (long long)gridDim.x * kRowsBlock * ROWS;
     const int C = p.C;
+    auto weights = [&](int k) {
+        const int c = (k * NT + t) * V;
+        return load_pack<float, V>(p.w + (c < C ? c : 0));
+    };
+    constexpr bool kHeld = K * V <= 16;   // the weights stay in registers, else in L1
+    W held[kHeld ? K : 1];
+    if constexpr (kHeld)
+#pragma unroll
+        for (int k = 0; k < K; ++k) held[k] = weights(k);
     int turn = 0;
     // the loop runs by whole blocks: threads without a row take part in the reductions
 #pragma unroll 1
@@ -169,7 +178,8 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT) norm_kernel(const NormPar
         for (int k = 0; k < K; ++k) {
             const int c = (k * NT + t) * V;
             W w;
-            if (FP8 == 1) w = load_pack<float, V>(p.w + (c < C ? c : 0));
+            if constexpr (kHeld) w = held[k];
+            else if (FP8 == 1) w = weights(k);
 #pragma unroll
             for (int q = 0; q < ROWS; ++q) {
                 const long long i = i0 + q * kRowsBlock;
@@ -205,7 +215,9 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT) norm_kernel(const NormPar
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int c = (k * NT + t) * V;
-            const W w = load_pack<float, V>(p.w + (c < C ? c : 0));
+            W w;
+            if constexpr (kHeld) w = held[k];
+            else w = weights(k);
 #pragma unroll
             for (int q = 0; q < ROWS; ++q) {
                 const bool ok = i0 + q * kRowsBlock < p.rows && c < C;
@@ -235,9 +247,13 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT) norm_kernel(const NormPar
     }
 }
 
+// CTAs an SM: 24 warps and more for rows of up to 4096 (short rows live from warps: gradients of
+// B8 H16 T8192 d128 take 167 us by 32 warps and one row at a time, 190 by 24 and two), fewer and
+// with more registers for longer rows.
 template <typename IO, int V, int K, int NT, int ROWS, bool DRES>
-__global__ void __launch_bounds__(NT < 256 ? 256 : NT) norm_backward_kernel(const NormBackwardParams p) {
-    constexpr int kBlock = NT < 256 ? 256 : NT;
+__global__ void __launch_bounds__(NT <= 32 ? 256 : NT, NT <= 32 ? (K * V == 8 ? 5 : 2) : NT == 128 ? 6 : NT == 256 ? (K * V <= 16 ? 3 : 2) : 1)
+norm_backward_kernel(const NormBackwardParams p) {
+    constexpr int kBlock = NT <= 32 ? 256 : NT;
     constexpr int kRowsBlock = NT <= 32 ? kBlock / NT : 1;
     static_assert(NT <= 32 || NT == kBlock, "a row has part of a warp, a warp or a CTA");
     using X = Pack<IO, V>;
@@ -252,6 +268,10 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT) norm_backward_kernel(cons
     for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int j = 0; j < V; ++j) dw[k][j] = 0.f;
+    auto weights = [&](int k) {
+        const int c = (k * NT + t) * V;
+        return load_pack<float, V>(p.w + (c < C ? c : 0));
+    };
     int turn = 0;
 #pragma unroll 1
     for (long long base = (long long)blockIdx.x * kRowsBlock * ROWS; base < p.rows; base += stride) {
@@ -275,8 +295,7 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT) norm_backward_kernel(cons
         for (int q = 0; q < ROWS; ++q) sum[q] = make_float2(0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = (k * NT + t) * V;
-            const W w = load_pack<float, V>(p.w + (c < C ? c : 0));
+            const W w = weights(k);
 #pragma unroll
             for (int q = 0; q < ROWS; ++q)
 #pragma unroll
@@ -291,7 +310,7 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT) norm_backward_kernel(cons
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int c = (k * NT + t) * V;
-            const W w = load_pack<float, V>(p.w + (c < C ? c : 0));
+            const W w = weights(k);
 #pragma unroll
             for (int q = 0; q < ROWS; ++q) {
                 const long long i = i0 + q * kRowsBlock;
@@ -386,7 +405,7 @@ void fill_rows(P &p, const A &a) {
 
 template <typename IO, int V, int K, int NT, int ROWS, bool RES, int FP8>
 cudaError_t launch_forward(const NormArgs &a) {
-    constexpr int kBlock = NT < 256 ? 256 : NT, kRowsBlock = NT <= 32 ? kBlock / NT : 1;
+    constexpr int kBlock = NT <= 32 ? 256 : NT, kRowsBlock = NT <= 32 ? kBlock / NT : 1;
     NormParams p;
     p.x = a.x; p.residual = a.residual; p.w = a.w;
     p.h = a.h; p.y = a.y; p.scales = a.scales;
@@ -402,6 +421,7 @@ cudaError_t launch_forward(const NormArgs &a) {
 
 template <typename IO, int V, int K, int NT, int ROWS>
 cudaError_t forward_kind(const NormArgs &a) {
+    // C > 1024 of vectors comes here by kind; the others take any
     if (!a.fp8)
         return a.residual ? launch_forward<IO, V, K, NT, ROWS, true, 0>(a) : launch_forward<IO, V, K, NT, ROWS, false, 0>(a);
     if constexpr (V == 8 && NT >= 16) {
@@ -414,27 +434,34 @@ cudaError_t forward_kind(const NormArgs &a) {
 template <typename IO>
 cudaError_t forward_io(const NormArgs &a) {
     const int C = a.C;
+    constexpr int M = sizeof(IO) == 2 ? 2 : 1;   // rows at a time by the registers they take
     if (C % 8) {
         if (C <= 256) return forward_kind<IO, 1, 8, 32, 1>(a);
-        if (C <= 2048) return forward_kind<IO, 1, 8, 256, 1>(a);
+        if (C <= 1024) return forward_kind<IO, 1, 4, 256, M>(a);
+        if (C <= 2048) return forward_kind<IO, 1, 8, 256, M>(a);
         if (C <= 8192) return forward_kind<IO, 1, 8, 1024, 1>(a);
         return forward_kind<IO, 1, 16, 1024, 1>(a);
     }
-    constexpr int M = sizeof(IO) == 2 ? 2 : 1;   // rows at a time by the registers they take
     if (C <= 64) return forward_kind<IO, 8, 1, 8, 2 * M>(a);
     if (C <= 128) return forward_kind<IO, 8, 1, 16, 2 * M>(a);
     if (C <= 256) return forward_kind<IO, 8, 1, 32, 2 * M>(a);
     if (C <= 512) return forward_kind<IO, 8, 2, 32, M>(a);
     if (C <= 1024) return forward_kind<IO, 8, 4, 32, 1>(a);
-    if (C <= 2048) return forward_kind<IO, 8, 1, 256, 2 * M>(a);
-    if (C <= 4096) return forward_kind<IO, 8, 2, 256, M>(a);
+    // 16384 x 2048 bf16: with a residual 48 us by 256 threads and several rows at a time (52 by 128);
+    // without one 30 us by 128 threads (35 by 256), to e4m3 44 us by 128 and one row (54 by 256)
+    if (C <= 2048) {
+        if (a.fp8) return forward_kind<IO, 8, 2, 128, 1>(a);
+        return a.residual ? forward_kind<IO, 8, 1, 256, 2 * M>(a) : forward_kind<IO, 8, 2, 128, M>(a);
+    }
+    // 32768 x 4096 bf16: with a residual 173 us one row at a time (189 two), without one 91 us two (108 one)
+    if (C <= 4096) return a.residual ? forward_kind<IO, 8, 2, 256, 1>(a) : forward_kind<IO, 8, 2, 256, M>(a);
     if (C <= 8192) return forward_kind<IO, 8, 4, 256, 1>(a);
     return forward_kind<IO, 8, 4, 512, 1>(a);
 }
 
 template <typename IO, int V, int K, int NT, int ROWS, bool DRES>
 cudaError_t launch_backward(const NormBackwardArgs &a) {
-    constexpr int kBlock = NT < 256 ? 256 : NT, kRowsBlock = NT <= 32 ? kBlock / NT : 1;
+    constexpr int kBlock = NT <= 32 ? 256 : NT, kRowsBlock = NT <= 32 ? kBlock / NT : 1;
     NormBackwardParams p;
     p.h = a.h; p.dy = a.dy; p.dres = a.dres; p.w = a.w;
     p.dx = a.dx; p.partial = a.partial;
@@ -463,21 +490,23 @@ cudaError_t backward_kind(const NormBackwardArgs &a) {
 template <typename IO>
 cudaError_t backward_io(const NormBackwardArgs &a) {
     const int C = a.C;
+    constexpr int M = sizeof(IO) == 2 ? 2 : 1;
     if (C % 8) {
         if (C <= 256) return backward_kind<IO, 1, 8, 32, 1>(a);
+        if (C <= 1024) return backward_kind<IO, 1, 4, 256, M>(a);
         if (C <= 2048) return backward_kind<IO, 1, 8, 256, 1>(a);
         if (C <= 8192) return backward_kind<IO, 1, 8, 1024, 1>(a);
         return backward_kind<IO, 1, 16, 1024, 1>(a);
     }
-    constexpr int M = sizeof(IO) == 2 ? 2 : 1;
-    if (C <= 64) return backward_kind<IO, 8, 1, 8, M>(a);
-    if (C <= 128) return backward_kind<IO, 8, 1, 16, M>(a);
-    if (C <= 256) return backward_kind<IO, 8, 1, 32, M>(a);
+    if (C <= 64) return backward_kind<IO, 8, 1, 8, 1>(a);
+    if (C <= 128) return backward_kind<IO, 8, 1, 16, 1>(a);
+    if (C <= 256) return backward_kind<IO, 8, 1, 32, 1>(a);
     if (C <= 512) return backward_kind<IO, 8, 2, 32, 1>(a);
-    if (C <= 2048) return backward_kind<IO, 8, 1, 256, 2 * M>(a);
-    if (C <= 4096) return backward_kind<IO, 8, 2, 256, M>(a);
-    if (C <= 8192) return backward_kind<IO, 8, 2, 512, 1>(a);
-    return backward_kind<IO, 8, 2, 1024, 1>(a);
+    if (C <= 1024) return backward_kind<IO, 8, 1, 128, 1>(a);
+    if (C <= 2048) return backward_kind<IO, 8, 2, 128, 1>(a);
+    if (C <= 4096) return backward_kind<IO, 8, 2, 256, 1>(a);
+    if (C <= 8192) return backward_kind<IO, 8, 4, 256, 1>(a);
+    return backward_kind<IO, 8, 4, 512, 1>(a);
 }
 
 }  // namespace
