@@ -201,7 +201,7 @@ def _check(status: int, where: str):
 def _need(t, shape, dtype, name):
     if t is None:
         raise ValueError(f"{name} is required")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
@@ -653,7 +653,22 @@ def _int32(**sizes):
 
 def _on(stream):
     """Allocations made inside belong to the call's stream."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return _HERE_AND_NOW if stream is None else torch.cuda.stream(stream)
+
+
+_HERE_AND_NOW = contextlib.nullcontext()
+
+
+def _raw_stream(t: torch.Tensor, stream) -> int:
+    """The call's cudaStream_t.  (The raw query: a one-token call is bound by its host side, and
+    torch.cuda.current_stream alone takes 2 us.)"""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(t.device.index) if t.is_cuda else 0
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def linear_scan(x, gate, *, state=None, init_state: bool | None = None, blend: bool = False,
@@ -686,8 +701,8 @@ def linear_scan(x, gate, *, state=None, init_state: bool | None = None, blend: b
     _need(state, (B, C), torch.float32, "state")
     _need(h, (B, T, C), dt, "h")
     flags = (FLAG_INIT_STATE if init_state else 0) | (SCAN_BLEND if blend else 0)
-    st = library().la_linear_scan(dtype, B, T, C, _ptr(x), _ptr(gate), _ptr(state), _ptr(h), _ptr(kept),
-                                  flags, _stream_handle(x.device, stream))
+    st = library().la_linear_scan(dtype, B, T, C, _at(x), _at(gate), _at(state), _at(h), _at(kept),
+                                  flags, _raw_stream(x, stream))
     _check(st, "la_linear_scan")
     return (h, state, kept) if checkpoints else (h, state)
 
@@ -722,9 +737,9 @@ def linear_scan_varlen(x, gate, cu_seqlens, *, state=None, init_state: bool | No
     _need(state, (N, C), torch.float32, "state")
     _need(h, (T, C), dt, "h")
     flags = (FLAG_INIT_STATE if init_state else 0) | (SCAN_BLEND if blend else 0)
-    st = library().la_linear_scan_varlen(dtype, N, T, C, _ptr(cu_seqlens), _ptr(x), _ptr(gate), _ptr(state),
-                                         _ptr(h), flags, _ptr(ws), ws.numel(),
-                                         _stream_handle(x.device, stream))
+    st = library().la_linear_scan_varlen(dtype, N, T, C, _at(cu_seqlens), _at(x), _at(gate), _at(state),
+                                         _at(h), flags, _at(ws), ws.numel(),
+                                         _raw_stream(x, stream))
     _check(st, "la_linear_scan_varlen")
     return h, state
 
@@ -743,8 +758,8 @@ def linear_scan_step(x, gate, state, *, blend: bool = False, h=None, stream=None
         with _on(stream):
             h = torch.empty_like(x)
     _need(h, (N, C), dt, "h")
-    st = library().la_linear_scan_step(dtype, N, C, _ptr(x), _ptr(gate), _ptr(state), _ptr(h),
-                                       SCAN_BLEND if blend else 0, _stream_handle(x.device, stream))
+    st = library().la_linear_scan_step(dtype, N, C, _at(x), _at(gate), _at(state), _at(h),
+                                       SCAN_BLEND if blend else 0, _raw_stream(x, stream))
     _check(st, "la_linear_scan_step")
     return h
 
@@ -778,10 +793,10 @@ def linear_scan_backward(x, gate, dh, *, state0=None, checkpoints=None, dstate=N
         dgate = torch.empty_like(gate) if need_dgate else None
         dstate0 = torch.empty(B, C, device=x.device, dtype=torch.float32) if need_dstate0 else None
         ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device) if nbytes else None
-    st = library().la_linear_scan_backward(dtype, B, T, C, _ptr(x), _ptr(gate), _ptr(state0), _ptr(checkpoints),
-                                           _ptr(dh), _ptr(dstate), _ptr(dx), _ptr(dgate), _ptr(dstate0),
-                                           SCAN_BLEND if blend else 0, _ptr(ws), nbytes,
-                                           _stream_handle(x.device, stream))
+    st = library().la_linear_scan_backward(dtype, B, T, C, _at(x), _at(gate), _at(state0), _at(checkpoints),
+                                           _at(dh), _at(dstate), _at(dx), _at(dgate), _at(dstate0),
+                                           SCAN_BLEND if blend else 0, _at(ws), nbytes,
+                                           _raw_stream(x, stream))
     _check(st, "la_linear_scan_backward")
     return dx, dgate, dstate0
 
@@ -822,6 +837,20 @@ def rotary_frequencies(rotary_dim: int, *, base: float = 10000.0, scaling: str |
     return freqs.to(device), scale
 
 
+def _rotary(q, k, B, T, Hq, Hk, d, freqs, positions, start, scale, flags, yq, yk, stream):
+    dt = q.dtype
+    dtype = _io_dtype(q)
+    _need(q, q.shape, dt, "q")
+    if k is not None:
+        _need(k, k.shape, dt, "k")
+    _int32(B=B, T=T, start=start)
+    _need(freqs, (freqs.numel(),), torch.float64, "freqs")
+    st = library().la_rotary(dtype, B, T, Hq, Hk, d, 2 * freqs.numel(), _at(q), _at(k), _at(freqs),
+                             _at(positions), start, scale, _at(yq), _at(yk), flags, _raw_stream(q, stream))
+    _check(st, "la_rotary")
+    return yq if k is None else (yq, yk)
+
+
 def _rotary_sizes(t, d, name):
     """(token-major, B, T, H, d) of a [B, T, H*d] or [B, H, T, d] tensor."""
     if t.dim() == 3:
@@ -835,19 +864,13 @@ def _rotary_sizes(t, d, name):
     return False, t.shape[0], t.shape[2], t.shape[1], t.shape[3]
 
 
-def _rotary(q, k, freqs, d, positions, start, scale, interleaved, transpose, y_tokens, in_place, stream):
-    dt = q.dtype
-    dtype = _io_dtype(q)
+def _rotary_rows(q, k, freqs, d, positions, start, scale, flags, y_tokens, in_place, stream):
     x_tokens, B, T, Hq, d = _rotary_sizes(q, d, "q")
-    _need(q, q.shape, dt, "q")
     Hk = 0
     if k is not None:
         kt, kB, kT, Hk, _ = _rotary_sizes(k, d, "k")
         if (kt, kB, kT) != (x_tokens, B, T):
             raise ValueError(f"k: expected q's layout, batch and length, got {tuple(k.shape)}")
-        _need(k, k.shape, dt, "k")
-    _int32(B=B, T=T, start=int(start))
-    _need(freqs, (freqs.numel(),), torch.float64, "freqs")
     if positions is not None:
         _need(positions, (B, T), torch.int32, "positions")
     if in_place:
@@ -856,16 +879,11 @@ def _rotary(q, k, freqs, d, positions, start, scale, interleaved, transpose, y_t
         yq, yk = q, k
     else:
         def out(H):
-            return torch.empty((B, T, H * d) if y_tokens else (B, H, T, d), device=q.device, dtype=dt)
+            return torch.empty((B, T, H * d) if y_tokens else (B, H, T, d), device=q.device, dtype=q.dtype)
         with _on(stream):
-            yq, yk = out(Hq), (out(Hk) if Hk else None)
-    flags = ((ROT_INTERLEAVED if interleaved else 0) | (ROT_TRANSPOSE if transpose else 0)
-             | (ROT_X_TOKENS if x_tokens else 0) | (ROT_Y_TOKENS if y_tokens else 0))
-    st = library().la_rotary(dtype, B, T, Hq, Hk, d, 2 * freqs.numel(), _ptr(q), _ptr(k), _ptr(freqs),
-                             _ptr(positions), int(start), float(scale), _ptr(yq), _ptr(yk), flags,
-                             _stream_handle(q.device, stream))
-    _check(st, "la_rotary")
-    return yq if k is None else (yq, yk)
+            yq, yk = out(Hq), (None if k is None else out(Hk))
+    flags |= (ROT_X_TOKENS if x_tokens else 0) | (ROT_Y_TOKENS if y_tokens else 0)
+    return _rotary(q, k, B, T, Hq, Hk, d, freqs, positions, int(start), float(scale), flags, yq, yk, stream)
 
 
 def rotary(q, k=None, *, freqs, d: int | None = None, positions=None, start: int = 0, scale: float = 1.0,
@@ -878,19 +896,27 @@ def rotary(q, k=None, *, freqs, d: int | None = None, positions=None, start: int
     positions: int32 [B, T], or None: start + t; packed sequences are B = 1 with positions.
     ``in_place`` (head-major inputs) turns q and k where they lie.  Returns y_q, or (y_q, y_k).
     """
-    return _rotary(q, k, freqs, d, positions, start, scale, interleaved, False, False, in_place, stream)
+    return _rotary_rows(q, k, freqs, d, positions, start, scale, ROT_INTERLEAVED if interleaved else 0, False,
+                        in_place, stream)
 
 
 def rotary_step(q, k=None, *, freqs, d: int, positions, scale: float = 1.0, interleaved: bool = False,
                 stream=None):
     """One new token of N sequences: q [N, H*d], k [N, H_k*d], positions int32 [N].  Returns y_q
     [N, H, d] (the q of ``decode_step``), or (y_q, y_k)."""
-    if q.dim() != 2 or (k is not None and k.dim() != 2):
+    if q.dim() != 2 or (k is not None and (k.dim() != 2 or k.shape[0] != q.shape[0])):
         raise ValueError("q and k must be [N, H*d]")
-    _need(positions, (q.shape[0],), torch.int32, "positions")
-    y = _rotary(q.unsqueeze(1), None if k is None else k.unsqueeze(1), freqs, d, positions.unsqueeze(1), 0,
-                scale, interleaved, False, False, False, stream)
-    return y.squeeze(2) if k is None else (y[0].squeeze(2), y[1].squeeze(2))
+    N, Cq = q.shape
+    Ck = 0 if k is None else k.shape[1]
+    if not d or Cq % d or Ck % d:
+        raise ValueError("d must divide the last dimension of q and k")
+    _need(positions, (N,), torch.int32, "positions")
+    with _on(stream):
+        yq = torch.empty((N, Cq // d, d), device=q.device, dtype=q.dtype)
+        yk = None if k is None else torch.empty((N, Ck // d, d), device=q.device, dtype=q.dtype)
+    # a token's rows [H*d] are its head rows [H, 1, d]
+    return _rotary(q, k, N, 1, Cq // d, Ck // d, d, freqs, positions, 0, float(scale),
+                   (ROT_INTERLEAVED if interleaved else 0) | ROT_X_TOKENS, yq, yk, stream)
 
 
 def rotary_backward(dq, dk=None, *, freqs, d: int | None = None, positions=None, start: int = 0,
@@ -899,7 +925,8 @@ def rotary_backward(dq, dk=None, *, freqs, d: int | None = None, positions=None,
     """Gradients of ``rotary`` (the transposed rotation): dq, dk [B, H, T, d] (or [B, T, H*d] with
     ``d``), the other arguments as for ``rotary``.  Returns the gradients of q and k, head-major or
     (``token_major``) [B, T, H*d] as the projections gave them."""
-    return _rotary(dq, dk, freqs, d, positions, start, scale, interleaved, True, token_major, in_place, stream)
+    return _rotary_rows(dq, dk, freqs, d, positions, start, scale,
+                        ROT_TRANSPOSE | (ROT_INTERLEAVED if interleaved else 0), token_major, in_place, stream)
 
 
 def _rms_norm(x, B, H, T, C, w, residual, residual_out, eps, fp8, group, y_shape, scale_shape, stream):
@@ -921,9 +948,9 @@ def _rms_norm(x, B, H, T, C, w, residual, residual_out, eps, fp8, group, y_shape
             residual_out = torch.empty_like(x)
     if residual is not None:
         _need(residual_out, x.shape, dt, "residual_out")
-    st = library().la_rms_norm(dtype, B, H, T, C, _ptr(x), _ptr(residual), _ptr(w), float(eps),
-                               _ptr(residual_out), _ptr(y), _ptr(scales), int(group),
-                               NORM_FP8 if fp8 else 0, _stream_handle(x.device, stream))
+    st = library().la_rms_norm(dtype, B, H, T, C, _at(x), _at(residual), _at(w), float(eps),
+                               _at(residual_out), _at(y), _at(scales), int(group),
+                               NORM_FP8 if fp8 else 0, _raw_stream(x, stream))
     _check(st, "la_rms_norm")
     out = (y,) + ((scales,) if fp8 else ()) + ((residual_out,) if residual is not None else ())
     return out[0] if len(out) == 1 else out
@@ -974,9 +1001,9 @@ def _rms_norm_backward(h, B, H, T, C, w, dy, dy_shape, dresidual, eps, stream):
     with _on(stream):
         dx, dw = torch.empty_like(h), torch.empty_like(w)
         ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=h.device)
-    st = library().la_rms_norm_backward(dtype, B, H, T, C, _ptr(h), _ptr(w), float(eps), _ptr(dy),
-                                        _ptr(dresidual), _ptr(dx), _ptr(dw), _ptr(ws), ws.numel(),
-                                        _stream_handle(h.device, stream))
+    st = library().la_rms_norm_backward(dtype, B, H, T, C, _at(h), _at(w), float(eps), _at(dy),
+                                        _at(dresidual), _at(dx), _at(dw), _at(ws), ws.numel(),
+                                        _raw_stream(h, stream))
     _check(st, "la_rms_norm_backward")
     return dx, dw
 
