@@ -147,11 +147,6 @@ size_t norm_backward_partial_bytes(long long rows, int C);
 cudaError_t launch_scan(const ScanArgs &a);
 cudaError_t launch_scan_step(const ScanArgs &a);
 cudaError_t launch_scan_backward(const ScanBackwardArgs &a);
-// The same by TMA (scan_tma.cu), and whether a call's rows can come that way.
-bool scan_tma_takes(const ScanArgs &a);
-bool scan_tma_takes(const ScanBackwardArgs &a);
-cudaError_t launch_scan_tma(const ScanArgs &a);
-cudaError_t launch_scan_backward_tma(const ScanBackwardArgs &a);
 // Packed sequences: the code of every row, checks of the offsets; the state of every empty
 // sequence is zeroed (zero_state: the state, or nullptr to leave it).
 size_t scan_codes_bytes(int T);

@@ -11,28 +11,40 @@
 //   l_t = dh_t + a_{t+1} l_{t+1},   dx_t = l_t (or (1 - a_t) l_t),
 //   da_t = l_t h_{t-1} (or l_t (h_{t-1} - x_t)),   dh_0 = a_1 l_1.
 //
-// A run of rows acts on the state in front of it as h -> P h + H (P the product of its
-// gates, H its own result from a zero state), and two runs join by
-// (P, H) o (P', H') = (P P', P' H + H'), so the time axis is cut and joined again:
-//   thread   S consecutive rows of V neighbouring channels, walked one after the other;
-//   warp     the 32 / LC threads that hold the same channels join by shuffles;
-//   CTA      its 8 warps join through shared memory (one thread a channel);
-//   cluster  K CTAs take consecutive tiles of the same channels and exchange (P, H) through
-//            distributed shared memory, one cluster barrier a step; every CTA folds all K, so
-//            all of them carry the state of the step's last row into the next one.
-// Once a thread knows the state in front of its rows it walks them again from it, with the
-// plain recurrence, and stores.  Everything is in fp32 and in a fixed order (no atomics, no
-// waiting on other clusters): results are the same bits from call to call.
+// A run of rows acts on the state in front of it as h -> P h + H (P the product of its gates, H
+// its own result from a zero state), and two runs join by (P, H) o (P', H') = (P P', P' H + H'),
+// so the time axis is cut into runs and joined again.  A tile is 8 S rows of 32 V channels; of the
+// CTA's eight warps each walks S of them, each lane V neighbouring channels (as packed fp32 pairs
+// for V = 2), so no shuffle is needed, and sequence starts and the end of the rows are decided
+// for whole warps.  A step:
 //
-// Bound by HBM: 8 (bf16) or 12 (fp32) bytes an element and two or three operations.  Each
-// input is read once: a thread's rows arrive by cp.async in its own slots of a ring in shared
-// memory, kStages tiles ahead, and stay in registers between the two walks.  The backward
-// pass needs h_{t-1}: the forward pass keeps the state in front of every 32nd row
-// (`checkpoints`, 1/32 of a fp32 h), from which a tile's rows are walked again on chip, so
-// the backward pass too reads each input once.
+//   walk 1          a warp takes its rows of the tile to registers and forms (P, H)
+//   fold            one barrier; then every thread folds the eight runs of its channels itself:
+//                   what lies in front of its warp, and the whole tile.  The barrier also says
+//                   that all warps have taken their rows: TMA is asked for the tile STAGES steps
+//                   on, a box of gates, one of x (and of dh), into the same stage
+//   meet (K > 1)    the K CTAs of a cluster, which hold consecutive tiles, send their tile's run
+//                   to each other by st.async, whose bytes complete the receiver's barrier, and
+//                   all fold all K: each of them carries the state of the step's last row on
+//   walk 2          from the state in front of its rows each warp walks them again, with the
+//                   plain recurrence, and stores
+//
+// Everything is in fp32 and in a fixed order (no atomics): the same bits on every call.  Each
+// input is read once.  The backward pass needs h_{t-1}: the forward pass keeps the state in front
+// of every 32nd row (`checkpoints`, 1/32 of a fp32 h), from which a tile's rows are walked again
+// on chip.
+//
+// What bounds it: HBM where there are columns for every SM: forward B2 T32768 C2048 bf16, 128
+// CTAs of 32 channels, 168 us, 97 % of the copy rate (a first version with lanes copying their
+// own values, shuffles and a cluster barrier a step took 444).  A CTA's step is a chain of
+// latencies (barrier, shared-memory reads, fold: 1.0 to 1.3 us a tile), so with few columns the
+// time axis goes over K CTAs and walk 1 of the next step comes before walk 2 of this one (AHEAD):
+// the runs travel meanwhile (B1 T50001 C192 fp32: 32 us, floor 18; 42 without AHEAD).
 #include "scan_util.cuh"
+#include "tmap.cuh"
 #include "vec.cuh"
 
+#include <cmath>
 #include <initializer_list>
 #include <type_traits>
 
@@ -40,581 +52,726 @@ namespace la {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kSlots = 4;                      // steps whose runs can be on their way between ranks
 
-template <int BYTES>
-__device__ __forceinline__ void copy_async(void *dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(ptx::smem_u32(dst)), "l"(src), "n"(BYTES)
+// V neighbouring channels of one lane, as one (V = 1) or packed (V = 2) fp32 operand.
+template <int V>
+struct Lane;
+template <>
+struct Lane<1> {
+    float v;
+    static __device__ __forceinline__ Lane all(float x) { return {x}; }
+    static __device__ __forceinline__ Lane load(const float *p) { return {*p}; }
+    __device__ __forceinline__ void store(float *p) const { *p = v; }
+    __device__ __forceinline__ void store(__nv_bfloat16 *p) const { *p = __float2bfloat16_rn(v); }
+};
+template <>
+struct Lane<2> {
+    unsigned long long v;
+    static __device__ __forceinline__ Lane make(float a, float b) {
+        Lane r;
+        asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+        return r;
+    }
+    static __device__ __forceinline__ Lane all(float x) { return make(x, x); }
+    __device__ __forceinline__ float2 both() const {
+        float2 r;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+        return r;
+    }
+    static __device__ __forceinline__ Lane load(const float *p) {
+        const float2 f = *reinterpret_cast<const float2 *>(p);
+        return make(f.x, f.y);
+    }
+    __device__ __forceinline__ void store(float *p) const { *reinterpret_cast<float2 *>(p) = both(); }
+    __device__ __forceinline__ void store(__nv_bfloat16 *p) const {
+        const float2 f = both();
+        *reinterpret_cast<uint32_t *>(p) = ptx::pack_bf16x2(f.x, f.y);
+    }
+};
+__device__ __forceinline__ Lane<1> fma(Lane<1> a, Lane<1> b, Lane<1> c) { return {fmaf(a.v, b.v, c.v)}; }
+__device__ __forceinline__ Lane<1> mul(Lane<1> a, Lane<1> b) { return {a.v * b.v}; }
+__device__ __forceinline__ Lane<1> add(Lane<1> a, Lane<1> b) { return {a.v + b.v}; }
+__device__ __forceinline__ Lane<2> fma(Lane<2> a, Lane<2> b, Lane<2> c) {
+    Lane<2> r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ Lane<2> mul(Lane<2> a, Lane<2> b) {
+    Lane<2> r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ Lane<2> add(Lane<2> a, Lane<2> b) {
+    Lane<2> r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+// (1 - a) x with one rounding of the exact x - a x
+template <int V>
+__device__ __forceinline__ Lane<V> blended(Lane<V> a, Lane<V> x) {
+    return fma(mul(a, Lane<V>::all(-1.f)), x, x);
+}
+template <int V>
+__device__ __forceinline__ Lane<V> sub(Lane<V> a, Lane<V> b) {
+    return fma(b, Lane<V>::all(-1.f), a);
+}
+
+__device__ __forceinline__ Lane<1> pick(bool c, Lane<1> a, Lane<1> b) { return {c ? a.v : b.v}; }
+__device__ __forceinline__ Lane<2> pick(bool c, Lane<2> a, Lane<2> b) {
+    Lane<2> r;
+    r.v = c ? a.v : b.v;
+    return r;
+}
+
+// A lane's values as they lie in memory (half the registers for bf16), widened where used.
+template <typename IO, int V>
+struct Raw;
+template <int V>
+struct Raw<float, V> {
+    Lane<V> v;
+    __device__ __forceinline__ void load(const float *p) { v = Lane<V>::load(p); }
+    __device__ __forceinline__ void zero() { v = Lane<V>::all(0.f); }
+    __device__ __forceinline__ Lane<V> wide() const { return v; }
+};
+template <>
+struct Raw<__nv_bfloat16, 1> {
+    uint16_t v;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { v = *reinterpret_cast<const uint16_t *>(p); }
+    __device__ __forceinline__ void zero() { v = 0; }
+    __device__ __forceinline__ Lane<1> wide() const { return {__uint_as_float((uint32_t)v << 16)}; }
+};
+template <>
+struct Raw<__nv_bfloat16, 2> {
+    uint32_t v;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { v = *reinterpret_cast<const uint32_t *>(p); }
+    __device__ __forceinline__ void zero() { v = 0; }
+    __device__ __forceinline__ Lane<2> wide() const {   // bf16 -> fp32: the high half
+        return Lane<2>::make(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+    }
+};
+
+// (P, H) of a run of rows, one lane's channels.
+template <int V>
+struct alignas(8 * V) Run {
+    Lane<V> P, H;
+    static __device__ __forceinline__ Run none() { return {Lane<V>::all(1.f), Lane<V>::all(0.f)}; }
+};
+// To shared memory of CTA `rank` of the cluster; the bytes count towards its barrier `bar` (both
+// given by this CTA's own addresses).
+__device__ __forceinline__ uint32_t of_rank(uint32_t addr, uint32_t rank) {
+    uint32_t to;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(addr), "r"(rank));
+    return to;
+}
+__device__ __forceinline__ void send(uint32_t addr, uint32_t bar, uint32_t rank, const Run<1> &r) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(
+                     of_rank(addr, rank)),
+                 "f"(r.P.v), "f"(r.H.v), "r"(of_rank(bar, rank))
                  : "memory");
+}
+__device__ __forceinline__ void send(uint32_t addr, uint32_t bar, uint32_t rank, const Run<2> &r) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b64 [%0], {%1, %2}, [%3];" ::"r"(
+                     of_rank(addr, rank)),
+                 "l"(r.P.v), "l"(r.H.v), "r"(of_rank(bar, rank))
+                 : "memory");
+}
+__device__ __forceinline__ void send(uint32_t addr, uint32_t bar, uint32_t rank, int v) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.s32 [%0], %1, [%2];" ::"r"(of_rank(addr, rank)),
+                 "r"(v), "r"(of_rank(bar, rank))
+                 : "memory");
+}
+
+struct KernelParams {
+    CUtensorMap gate, x;     // [B][T][C], boxes of a tile: TT rows x CH channels
+    ScanParams s;
+    unsigned *err;
+};
+struct BackwardKernelParams {
+    CUtensorMap gate, x, dh;
+    BackwardParams b;
+    unsigned *err;
+};
+
+// Shape: V channels a lane, E elements a thread.
+template <int V_, int E_>
+struct Shape {
+    static constexpr int V = V_, E = E_, S = E / V, CH = 32 * V, TT = kWarps * S;
+    static_assert(TT <= 256 && S <= 32, "a box has at most 256 rows; a warp's row codes fit its lanes");
+};
+constexpr uint32_t whole(uint32_t n) { return (n + 127) / 128 * 128; }
+
+// One stage of the ring: the tile's gates, x (dh), then packed batches' row codes or the
+// backward pass's checkpoint rows (one for each 32 rows).
+template <typename IO, typename SH, bool TMA>
+struct ScanStage {
+    static constexpr uint32_t kGate = SH::TT * SH::CH * sizeof(float), kX = SH::TT * SH::CH * (TMA ? sizeof(IO) : 4);
+    static constexpr uint32_t bytes(bool packed) { return whole(kGate + kX + (packed ? SH::TT * 4 : 0)); }
+};
+template <typename IO, typename SH, bool TMA>
+struct BackwardStage {
+    static constexpr uint32_t kGate = SH::TT * SH::CH * sizeof(float), kX = SH::TT * SH::CH * (TMA ? sizeof(IO) : 4);
+    static constexpr uint32_t kKept = kGate + 2 * kX;
+    static constexpr int kSpans = SH::TT / kScanCheckpoint;
+    static constexpr uint32_t bytes() { return whole(kKept + kSpans * SH::CH * sizeof(float)); }
+};
+
+// Rows that TMA cannot take (V = 1): every lane copies its own channel's values into its own
+// places of the ring, 4 bytes at a time, and reads nothing else, so it waits for its own copies
+// alone.  A bf16 value comes with the aligned word it lies in, of which the lane picks its half;
+// the first and the last word of a tensor could reach beyond it, so the tiles that hold those
+// take their values singly.
+__device__ __forceinline__ void copy_word(void *dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+// n rows of a lane's channel, `pitch` values apart, to places `to` a row apart.
+template <int ROW>
+__device__ __forceinline__ void copy_rows(uint32_t *to, const float *from, long long pitch, int n, bool) {
+#pragma unroll 4
+    for (int s = 0; s < n; ++s) copy_word(to + s * ROW, from + s * pitch);
+}
+template <int ROW>
+__device__ __forceinline__ void copy_rows(uint32_t *to, const __nv_bfloat16 *from, long long pitch, int n, bool edge) {
+    const uint16_t *at = reinterpret_cast<const uint16_t *>(from);
+    if (edge) {
+        for (int s = 0; s < n; ++s) to[s * ROW] = at[s * pitch] * 0x10001u;   // in both halves
+    } else {
+#pragma unroll 4
+        for (int s = 0; s < n; ++s)
+            copy_word(to + s * ROW, reinterpret_cast<const void *>(reinterpret_cast<uintptr_t>(at + s * pitch) & ~(uintptr_t)3));
+    }
+}
+// Row s of copied values: `from` is the tensor's place of the lane's row 0.
+__device__ __forceinline__ void pick_word(Raw<float, 1> &x, uint32_t word, const float *, long long) {
+    x.v.v = __uint_as_float(word);
+}
+__device__ __forceinline__ void pick_word(Raw<__nv_bfloat16, 1> &x, uint32_t word, const __nv_bfloat16 *from, long long off) {
+    const bool high = (reinterpret_cast<uintptr_t>(from) / 2 + (uintptr_t)off) & 1;
+    x.v = (uint16_t)(high ? word >> 16 : word);
+}
 
-// Shape of a kernel: V channels a thread (one vector load), LC threads side by side, E
-// elements a thread.
-template <int V_, int LC_, int E_>
-struct Shape {
-    static constexpr int V = V_, LC = LC_, E = E_;
-    static constexpr int S = E / V;                 // rows a thread
-    static constexpr int CH = LC * V;               // channels a CTA
-    static constexpr int G = kThreads / LC;         // row groups of a CTA
-    static constexpr int TT = G * S;                // rows a tile
-    static constexpr int SUB = 32 / LC;             // row groups of a warp
-};
-
-// One CTA's exchange area in dynamic shared memory, behind the ring.
-template <int CH>
+// Shared memory: the ring of stages, then this, then (on 16 bytes) Run slot[kSlots][K][32].
+template <int V, int STAGES>
 struct Exchange {
-    // by the step's parity, so that a step's writes never meet the last one's reads:
-    float2 warp[2][kWarps][CH];   // (P, H) of each warp, then those of all earlier warps
+    Run<V> warp[2][kWarps][32];   // by the step's parity
+    Lane<V> back[2][kWarps][32];  // backward pass: M
+    uint64_t full[STAGES];
+    uint64_t met[kSlots];         // the step's runs of all ranks are here
     int reset[2][kWarps];         // packed: a sequence starts in the warp's rows
-    float carry[CH];              // state in front of the tile
-    int slot_reset[2][kMaxCluster];
-    // followed by float2 slot[2][K][CH]: (P, H) of each rank's tile
+    int slot_reset[kSlots][kMaxCluster];
+    int abort;
 };
+template <int V, int STAGES>
+constexpr size_t exchange_bytes() { return (sizeof(Exchange<V, STAGES>) + 15) / 16 * 16; }
 
-__device__ __forceinline__ void store_cluster(uint32_t addr, uint32_t rank, float a, float b) {
-    uint32_t to;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(addr), "r"(rank));
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(a), "f"(b) : "memory");
-}
-__device__ __forceinline__ void store_cluster(uint32_t addr, uint32_t rank, int a) {
-    uint32_t to;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(addr), "r"(rank));
-    asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(to), "r"(a) : "memory");
-}
-template <typename IO, typename SH, int STAGES>
-constexpr size_t scan_ring_bytes() {
-    return SH::V == 1 ? 0 : (size_t)STAGES * kThreads * SH::E * (sizeof(float) + sizeof(IO));
-}
-template <typename IO, typename SH, int STAGES>
-constexpr size_t backward_ring_bytes() {
-    return SH::V == 1 ? 0
-                      : (size_t)STAGES * kThreads * (SH::E * (sizeof(float) + 2 * sizeof(IO)) + SH::V * sizeof(float));
-}
-template <typename SH>
-size_t exchange_bytes(int K) {
-    return sizeof(Exchange<SH::CH>) + (K > 1 ? (size_t)2 * K * SH::CH * sizeof(float2) : 0);
-}
-
-// Two CTAs an SM: the ring's bytes in flight of one cover the other's barriers.  Odd channel
-// counts (V = 1) have no 4-byte aligned rows for cp.async: their rows are loaded straight into
-// registers.
-template <typename IO, typename SH, int STAGES, bool BLEND, bool PACKED>
-__global__ void __launch_bounds__(kThreads, 2) scan_kernel(const ScanParams p) {
-    constexpr int V = SH::V, LC = SH::LC, S = SH::S, CH = SH::CH, TT = SH::TT, SUB = SH::SUB;
-    constexpr bool ASYNC = V > 1;
-    using XV = Pack<IO, V>;
-    using AV = Pack<float, V>;
-    extern __shared__ __align__(16) unsigned char smem[];
-    AV *ring_a = reinterpret_cast<AV *>(smem);                               // [STAGES][S][kThreads]
-    XV *ring_x = reinterpret_cast<XV *>(ring_a + (ASYNC ? STAGES * S * kThreads : 0));
-    auto *ex = reinterpret_cast<Exchange<CH> *>(smem + scan_ring_bytes<IO, SH, STAGES>());
-    float2 *slots = reinterpret_cast<float2 *>(ex + 1);
-
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int lc = tid % LC, grp = tid / LC;
-    const int K = p.K, rank = blockIdx.x % K;
-    const long long col = blockIdx.x / K;
-    const long long b = col / p.blocks;
-    const long long cb = (col % p.blocks) * CH, c0 = cb + lc * V;
-    const bool act = c0 < p.C;
-    const long long T = p.T, C = p.C;
-    const IO *xb = static_cast<const IO *>(p.x) + b * T * C + c0;
-    const float *ab = p.gate + b * T * C + c0;
-    IO *hb = p.h ? static_cast<IO *>(p.h) + b * T * C + c0 : nullptr;
-
-    auto first_row = [&](int step) { return ((long long)step * K + rank) * TT + (long long)grp * S; };
-    auto fetch = [&](int step) {
-        if constexpr (ASYNC) {
-            const long long t0 = first_row(step);
-            AV *sa = ring_a + (step % STAGES) * S * kThreads + tid;
-            XV *sx = ring_x + (step % STAGES) * S * kThreads + tid;
-            if (act && step < p.steps) {
-#pragma unroll
-                for (int s = 0; s < S; ++s)
-                    if (t0 + s < T) {
-                        copy_async<sizeof(AV)>(sa + s * kThreads, ab + (t0 + s) * C);
-                        copy_async<sizeof(XV)>(sx + s * kThreads, xb + (t0 + s) * C);
-                    }
-            }
-            copy_commit();
-        }
-    };
-    // thread `tid` < CH folds channel cb + tid; its running state
-    const bool folds = tid < CH;
-    float run = 0.f;
-    if (!PACKED && folds && cb + tid < C && p.state_in) run = p.state_in[b * C + cb + tid];
-#pragma unroll
-    for (int i = 0; i < STAGES; ++i) fetch(i);
+// Barriers and the cluster's start; the whole CTA.
+template <int V, int STAGES>
+__device__ __forceinline__ void start_exchange(Exchange<V, STAGES> *ex, int K, int askers) {
+    const int tid = threadIdx.x;
+    if (tid < STAGES) ptx::mbar_init(&ex->full[tid], askers);
+    if (tid < kSlots) ptx::mbar_init(&ex->met[tid], 1);
+    if (tid == 0) ex->abort = 0;
+    ptx::fence_mbar_init();
     if (K > 1) {   // every CTA of the cluster runs before the first store to its shared memory
         cluster_arrive();
         cluster_wait();
-    }
-
-    for (int step = 0; step < p.steps; ++step) {
-        const int par = step & 1;
-        const long long t0 = first_row(step);
-        AV a[S];
-        XV x[S];
-        int code[PACKED ? S : 1];
-        if constexpr (PACKED) {
-#pragma unroll
-            for (int s = 0; s < S; ++s) code[s] = 0;
-            if (t0 < T) {
-#pragma unroll
-                for (int s = 0; s < S; s += 4) {
-                    const int4 c = *reinterpret_cast<const int4 *>(p.codes + t0 + s);
-                    code[s] = c.x, code[s + 1] = c.y, code[s + 2] = c.z, code[s + 3] = c.w;
-                }
-            }
-        }
-        if constexpr (ASYNC) {
-            copy_wait<STAGES - 1>();
-            const AV *sa = ring_a + (step % STAGES) * S * kThreads + tid;
-            const XV *sx = ring_x + (step % STAGES) * S * kThreads + tid;
-#pragma unroll
-            for (int s = 0; s < S; ++s) {
-                a[s] = sa[s * kThreads];
-                x[s] = sx[s * kThreads];
-            }
-            fetch(step + STAGES);   // into the slots just read, which no other thread touches
-        } else {
-#pragma unroll
-            for (int s = 0; s < S; ++s)
-                if (act && t0 + s < T) {
-                    a[s] = *reinterpret_cast<const AV *>(ab + (t0 + s) * C);
-                    x[s] = *reinterpret_cast<const XV *>(xb + (t0 + s) * C);
-                }
-        }
-        // rows behind the end, and channels behind the last: a = 1, u = 0 leaves the state
-        if (!act || t0 + S > T) {
-#pragma unroll
-            for (int s = 0; s < S; ++s)
-                if (!act || t0 + s >= T)
-#pragma unroll
-                    for (int j = 0; j < V; ++j) a[s].v[j] = 1.f, x[s].v[j] = from_f32<IO>(0.f);
-        }
-        auto input = [&](int s, int j) {
-            const float u = to_f32(x[s].v[j]);
-            return BLEND ? (1.f - a[s].v[j]) * u : u;
-        };
-        // the thread's own rows: (P, H), and in a packed batch whether a sequence starts there.
-        // A first row starts from its sequence's slot; the row's h replaces its gate for the
-        // second walk, because the slot may be overwritten by then.
-        float P[V], H[V];
-        bool reset = false;
-#pragma unroll
-        for (int j = 0; j < V; ++j) P[j] = 1.f, H[j] = 0.f;
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-            if constexpr (PACKED) {
-                if (code[s] == 0) continue;
-                if (row_first(code[s])) {
-                    reset = true;
-#pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        const float h0 = (act && p.state_in) ? p.state_in[row_seq(code[s]) * C + c0 + j] : 0.f;
-                        H[j] = a[s].v[j] = fmaf(a[s].v[j], h0, input(s, j));
-                    }
-                    continue;
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                H[j] = fmaf(a[s].v[j], H[j], input(s, j));
-                P[j] *= a[s].v[j];
-            }
-        }
-        // join the warp's groups: inclusive, then shifted to what lies in front of the thread
-        int seen = reset;
-#pragma unroll
-        for (int off = LC; off < 32; off *= 2) {
-            const int before = PACKED ? __shfl_up_sync(~0u, seen, off) : 0;
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float Pb = __shfl_up_sync(~0u, P[j], off), Hb = __shfl_up_sync(~0u, H[j], off);
-                if (lane >= off && !(PACKED && seen)) {
-                    H[j] = fmaf(P[j], Hb, H[j]);
-                    P[j] *= Pb;
-                }
-            }
-            if (PACKED && lane >= off) seen |= before;
-        }
-        if (lane >= 32 - LC) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) ex->warp[par][warp][lc * V + j] = make_float2(P[j], H[j]);
-            if (PACKED && lane == 31) ex->reset[par][warp] = seen;
-        }
-        float Pf[V], Hf[V];
-        int seenf = 0;
-        if (SUB > 1) {
-            if (PACKED) seenf = __shfl_up_sync(~0u, seen, LC);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                Pf[j] = __shfl_up_sync(~0u, P[j], LC);
-                Hf[j] = __shfl_up_sync(~0u, H[j], LC);
-            }
-        }
-        if (SUB == 1 || lane < LC) {
-            seenf = 0;
-#pragma unroll
-            for (int j = 0; j < V; ++j) Pf[j] = 1.f, Hf[j] = 0.f;
-        }
+    } else {
         __syncthreads();
-        // join the warps: each slot gets what lies in front of it in the tile
-        float Pt = 1.f, Ht = 0.f;
-        int rt = 0;
-        if (folds) {
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float2 q = ex->warp[par][w][tid];
-                ex->warp[par][w][tid] = make_float2(Pt, Ht);
-                if (PACKED && ex->reset[par][w]) {
-                    rt = 1, Pt = q.x, Ht = q.y;
-                } else {
-                    Ht = fmaf(q.x, Ht, q.y);
-                    Pt *= q.x;
-                }
-            }
-        }
-        float cin = run;
-        if (K > 1) {
-            if (folds) {
-                const uint32_t at = ptx::smem_u32(slots + ((size_t)par * K + rank) * CH + tid);
-                for (int q = 0; q < K; ++q) store_cluster(at, q, Pt, Ht);
-                if (PACKED && tid == 0) {
-                    const uint32_t ar = ptx::smem_u32(&ex->slot_reset[par][rank]);
-                    for (int q = 0; q < K; ++q) store_cluster(ar, q, rt);
-                }
-            }
-            cluster_arrive();
-            cluster_wait();
-            if (folds) {
-                for (int q = 0; q < K; ++q) {
-                    if (q == rank) cin = run;
-                    const float2 e = slots[((size_t)par * K + q) * CH + tid];
-                    run = (PACKED && ex->slot_reset[par][q]) ? e.y : fmaf(e.x, run, e.y);
-                }
-            }
-        } else {
-            run = (PACKED && rt) ? Ht : fmaf(Pt, run, Ht);
-        }
-        if (folds) ex->carry[tid] = cin;
-        __syncthreads();
-        // the state in front of the thread's rows
-        float hv[V];
-        bool earlier = false;
-        if constexpr (PACKED)
-            for (int w = 0; w < warp; ++w) earlier |= ex->reset[par][w] != 0;
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const float2 w = ex->warp[par][warp][lc * V + j];
-            const float front = (PACKED && earlier) ? w.y : fmaf(w.x, ex->carry[lc * V + j], w.y);
-            hv[j] = (PACKED && seenf) ? Hf[j] : fmaf(Pf[j], front, Hf[j]);
-        }
-        if (p.ckpt && act && t0 < T && t0 % kScanCheckpoint == 0) {
-            AV k;
-#pragma unroll
-            for (int j = 0; j < V; ++j) k.v[j] = hv[j];
-            const long long rows = (T + kScanCheckpoint - 1) / kScanCheckpoint;
-            *reinterpret_cast<AV *>(p.ckpt + (b * rows + t0 / kScanCheckpoint) * C + c0) = k;
-        }
-        if (act) {
-#pragma unroll
-            for (int s = 0; s < S; ++s) {
-                if (t0 + s >= T) break;
-                if (PACKED && code[s] == 0) continue;
-                XV o;
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    hv[j] = (PACKED && row_first(code[s])) ? a[s].v[j] : fmaf(a[s].v[j], hv[j], input(s, j));
-                    o.v[j] = from_f32<IO>(hv[j]);
-                }
-                if (hb) *reinterpret_cast<XV *>(hb + (t0 + s) * C) = o;
-                if constexpr (PACKED) {
-                    if (row_last(code[s])) {
-#pragma unroll
-                        for (int j = 0; j < V; ++j) p.state_out[row_seq(code[s]) * C + c0 + j] = hv[j];
-                    }
-                }
-            }
-        }
-    }
-    if constexpr (ASYNC) copy_wait<0>();
-    if (!PACKED && rank == 0 && folds && cb + tid < C && p.state_out) p.state_out[b * C + cb + tid] = run;
-    if (K > 1) {   // no CTA may leave while another one's store to it is in flight
-        cluster_arrive();
-        cluster_wait();
     }
 }
-
-// The backward pass over dense batches: tiles from the last row to the first.  A run of rows
-// acts on m (the next row's a l) as m -> P m + M.
-template <typename IO, typename SH, int STAGES, bool BLEND>
-__global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(const BackwardParams p) {
-    constexpr int V = SH::V, LC = SH::LC, S = SH::S, CH = SH::CH, TT = SH::TT, SUB = SH::SUB;
-    constexpr bool ASYNC = V > 1;
-    constexpr int kGroups = kScanCheckpoint / S;   // row groups between two checkpoints
-    static_assert(kScanCheckpoint % S == 0 && TT % kScanCheckpoint == 0, "tiles hold whole checkpoint spans");
-    using XV = Pack<IO, V>;
-    using AV = Pack<float, V>;
-    extern __shared__ __align__(16) unsigned char smem[];
-    AV *ring_a = reinterpret_cast<AV *>(smem);                        // [STAGES][S][kThreads]
-    AV *ring_k = ring_a + (ASYNC ? STAGES * S * kThreads : 0);        // [STAGES][kThreads]
-    XV *ring_x = reinterpret_cast<XV *>(ring_k + (ASYNC ? STAGES * kThreads : 0));
-    XV *ring_d = ring_x + (ASYNC ? STAGES * S * kThreads : 0);
-    auto *ex = reinterpret_cast<Exchange<CH> *>(smem + backward_ring_bytes<IO, SH, STAGES>());
-    float2 *slots = reinterpret_cast<float2 *>(ex + 1);
-    __shared__ float2 fwd[2][kWarps][CH];   // (P, H) of each warp's rows forwards, then the state in front
-
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int lc = tid % LC, grp = tid / LC;
-    const int K = p.K, rank = blockIdx.x % K;
-    const long long col = blockIdx.x / K;
-    const long long b = col / p.blocks;
-    const long long cb = (col % p.blocks) * CH, c0 = cb + lc * V;
-    const bool act = c0 < p.C;
-    const long long T = p.T, C = p.C;
-    const long long rows = (T + kScanCheckpoint - 1) / kScanCheckpoint;
-    const long long tiles = (T + TT - 1) / TT;
-    const IO *xb = static_cast<const IO *>(p.x) + b * T * C + c0;
-    const IO *db = static_cast<const IO *>(p.dh) + b * T * C + c0;
-    const float *ab = p.gate + b * T * C + c0;
-    const float *kb = p.ckpt + b * rows * C + c0;
-    IO *ob = static_cast<IO *>(p.dx) + b * T * C + c0;
-    float *gb = p.dgate ? p.dgate + b * T * C + c0 : nullptr;
-    // a group at a checkpoint walks forwards from it; the others continue
-    const bool kept = grp % kGroups == 0;
-
-    // first row of the thread at a step; negative tiles (before the first row) hold none
-    auto first_row = [&](int step) {
-        return (tiles - 1 - ((long long)step * K + rank)) * TT + (long long)grp * S;
-    };
-    auto fetch = [&](int step) {
-        if constexpr (ASYNC) {
-            const long long t0 = first_row(step);
-            const int st = step % STAGES;
-            if (act && step < p.steps && t0 >= 0 && t0 < T) {
-#pragma unroll
-                for (int s = 0; s < S; ++s)
-                    if (t0 + s < T) {
-                        const int at = (st * S + s) * kThreads + tid;
-                        copy_async<sizeof(AV)>(ring_a + at, ab + (t0 + s) * C);
-                        copy_async<sizeof(XV)>(ring_x + at, xb + (t0 + s) * C);
-                        copy_async<sizeof(XV)>(ring_d + at, db + (t0 + s) * C);
-                    }
-                if (kept) copy_async<sizeof(AV)>(ring_k + st * kThreads + tid, kb + t0 / kScanCheckpoint * C);
-            }
-            copy_commit();
-        }
-    };
-    const bool folds = tid < CH;
-    float run = 0.f;
-    if (folds && cb + tid < C && p.dstate) run = p.dstate[b * C + cb + tid];
-#pragma unroll
-    for (int i = 0; i < STAGES; ++i) fetch(i);
-    if (K > 1) {   // every CTA of the cluster runs before the first store to its shared memory
-        cluster_arrive();
-        cluster_wait();
-    }
-
-    for (int step = 0; step < p.steps; ++step) {
-        const int par = step & 1;
-        const long long t0 = first_row(step);
-        const bool live = act && t0 >= 0 && t0 < T;
-        AV a[S], k;
-        XV x[S], d[S];
-        if constexpr (ASYNC) {
-            copy_wait<STAGES - 1>();
-            const int st = step % STAGES;
-#pragma unroll
-            for (int s = 0; s < S; ++s) {
-                const int at = (st * S + s) * kThreads + tid;
-                a[s] = ring_a[at];
-                x[s] = ring_x[at];
-                d[s] = ring_d[at];
-            }
-            k = ring_k[st * kThreads + tid];
-            fetch(step + STAGES);
-        } else if (live) {
-#pragma unroll
-            for (int s = 0; s < S; ++s)
-                if (t0 + s < T) {
-                    a[s] = *reinterpret_cast<const AV *>(ab + (t0 + s) * C);
-                    x[s] = *reinterpret_cast<const XV *>(xb + (t0 + s) * C);
-                    d[s] = *reinterpret_cast<const XV *>(db + (t0 + s) * C);
-                }
-            if (kept) k = *reinterpret_cast<const AV *>(kb + t0 / kScanCheckpoint * C);
-        }
-        if (!live || t0 + S > T) {
-#pragma unroll
-            for (int s = 0; s < S; ++s)
-                if (!live || t0 + s >= T)
-#pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        a[s].v[j] = 1.f;
-                        x[s].v[j] = from_f32<IO>(0.f);
-                        d[s].v[j] = from_f32<IO>(0.f);
-                    }
-        }
-        if (!live || !kept) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) k.v[j] = 0.f;
-        }
-        auto input = [&](int s, int j) {
-            const float u = to_f32(x[s].v[j]);
-            return BLEND ? (1.f - a[s].v[j]) * u : u;
-        };
-        // the thread's rows: P, forwards H (from the checkpoint where it has one), backwards M
-        float P[V], H[V], M[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) P[j] = 1.f, H[j] = k.v[j], M[j] = 0.f;
-#pragma unroll
-        for (int s = 0; s < S; ++s)
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                H[j] = fmaf(a[s].v[j], H[j], input(s, j));
-                P[j] *= a[s].v[j];
-            }
-#pragma unroll
-        for (int s = S - 1; s >= 0; --s)
-#pragma unroll
-            for (int j = 0; j < V; ++j) M[j] = a[s].v[j] * (to_f32(d[s].v[j]) + M[j]);
-        // join the warp's groups, forwards (a checkpoint ends the reach back) and backwards
-        float Pb[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) Pb[j] = P[j];
-        bool stop = kept;
-#pragma unroll
-        for (int off = LC; off < 32; off *= 2) {
-            const bool stop_before = __shfl_up_sync(~0u, (int)stop, off);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float Pf = __shfl_up_sync(~0u, P[j], off), Hf = __shfl_up_sync(~0u, H[j], off);
-                const float Pn = __shfl_down_sync(~0u, Pb[j], off), Mn = __shfl_down_sync(~0u, M[j], off);
-                if (lane >= off && !stop) {
-                    H[j] = fmaf(P[j], Hf, H[j]);
-                    P[j] *= Pf;
-                }
-                if (lane < 32 - off) {
-                    M[j] = fmaf(Pb[j], Mn, M[j]);
-                    Pb[j] *= Pn;
-                }
-            }
-            if (lane >= off) stop |= stop_before;
-        }
-        if (lane >= 32 - LC) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) fwd[par][warp][lc * V + j] = make_float2(P[j], H[j]);
-        }
-        if (lane < LC) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) ex->warp[par][warp][lc * V + j] = make_float2(Pb[j], M[j]);
-        }
-        if (lane == 31) ex->reset[par][warp] = stop;
-        // shifted: what lies in front of (forwards) and behind (backwards) the thread in the warp
-        float Pf[V], Hf[V], Pn[V], Mn[V];
-        bool stopf = false;
-        if (SUB > 1) {
-            stopf = __shfl_up_sync(~0u, (int)stop, LC);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                Pf[j] = __shfl_up_sync(~0u, P[j], LC);
-                Hf[j] = __shfl_up_sync(~0u, H[j], LC);
-                Pn[j] = __shfl_down_sync(~0u, Pb[j], LC);
-                Mn[j] = __shfl_down_sync(~0u, M[j], LC);
-            }
-        }
-        if (SUB == 1 || lane < LC) {
-            stopf = false;
-#pragma unroll
-            for (int j = 0; j < V; ++j) Pf[j] = 1.f, Hf[j] = 0.f;
-        }
-        if (SUB == 1 || lane >= 32 - LC) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) Pn[j] = 1.f, Mn[j] = 0.f;
-        }
-        __syncthreads();
-        float Pt = 1.f, Mt = 0.f;
-        if (folds) {
-#pragma unroll
-            for (int w = kWarps - 1; w >= 0; --w) {
-                const float2 q = ex->warp[par][w][tid];
-                ex->warp[par][w][tid] = make_float2(Pt, Mt);
-                Mt = fmaf(q.x, Mt, q.y);
-                Pt *= q.x;
-            }
-        } else if (tid >= kThreads - CH) {   // other threads join forwards
-            const int ch = tid - (kThreads - CH);
-            float state = 0.f;   // in front of the tile's first row: a checkpoint, in its own group
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float2 q = fwd[par][w][ch];
-                fwd[par][w][ch].y = state;
-                state = ex->reset[par][w] ? q.y : fmaf(q.x, state, q.y);
-            }
-        }
-        float cin = run;
-        if (K > 1) {
-            if (folds) {
-                const uint32_t at = ptx::smem_u32(slots + ((size_t)par * K + rank) * CH + tid);
-                for (int q = 0; q < K; ++q) store_cluster(at, q, Pt, Mt);
-            }
-            cluster_arrive();
-            cluster_wait();
-            if (folds) {
-                for (int q = 0; q < K; ++q) {
-                    if (q == rank) cin = run;
-                    const float2 e = slots[((size_t)par * K + q) * CH + tid];
-                    run = fmaf(e.x, run, e.y);
-                }
-            }
-        } else {
-            run = fmaf(Pt, run, Mt);
-        }
-        if (folds) ex->carry[tid] = cin;
-        __syncthreads();
-        if (live) {
-            float hv[S][V], m[V];
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float2 w = ex->warp[par][warp][lc * V + j];
-                m[j] = fmaf(Pn[j], fmaf(w.x, ex->carry[lc * V + j], w.y), Mn[j]);
-                const float front = fwd[par][warp][lc * V + j].y;
-                float h = kept ? k.v[j] : stopf ? Hf[j] : fmaf(Pf[j], front, Hf[j]);
-#pragma unroll
-                for (int s = 0; s < S; ++s) {
-                    hv[s][j] = h;
-                    h = fmaf(a[s].v[j], h, input(s, j));
-                }
-            }
-#pragma unroll
-            for (int s = S - 1; s >= 0; --s) {
-                XV o;
-                AV g;
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float l = to_f32(d[s].v[j]) + m[j], av = a[s].v[j];
-                    o.v[j] = from_f32<IO>(BLEND ? (1.f - av) * l : l);
-                    g.v[j] = l * (BLEND ? hv[s][j] - to_f32(x[s].v[j]) : hv[s][j]);
-                    m[j] = av * l;
-                }
-                if (t0 + s < T) {
-                    *reinterpret_cast<XV *>(ob + (t0 + s) * C) = o;
-                    if (gb) *reinterpret_cast<AV *>(gb + (t0 + s) * C) = g;
-                }
-            }
-        }
-    }
-    if constexpr (ASYNC) copy_wait<0>();
-    if (rank == 0 && folds && cb + tid < C && p.dstate0) p.dstate0[b * C + cb + tid] = run;
+// The end of the whole CTA.  After a wait that ran out, the copies still in flight get 10 ms to
+// land before the block's shared memory goes; and no CTA may leave while another one's store to
+// it is in flight.
+template <int V, int STAGES>
+__device__ __forceinline__ void end_exchange(Exchange<V, STAGES> *ex, int K) {
+    if (*(volatile int *)&ex->abort)
+        for (int i = 0; i < 1000; ++i) __nanosleep(10000);
     if (K > 1) {
         cluster_arrive();
         cluster_wait();
     }
+}
+
+// The tile's run to every rank, one rank a warp at a time.
+// A slot is used again kSlots = 4 steps later.  Its sender then has this CTA's run of at least two
+// steps before, which this CTA sent after it had read the slot.
+template <int V, int STAGES, bool RESETS>
+__device__ __forceinline__ void send_run(Exchange<V, STAGES> *ex, Run<V> *slots, int step, int K, int rank,
+                                         const Run<V> &all, bool reset) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slot = step % kSlots;
+    const uint32_t at = ptx::smem_u32(slots + ((size_t)slot * K + rank) * 32 + lane);
+    const uint32_t bar = ptx::smem_u32(&ex->met[slot]);
+    for (int to = warp; to < K; to += kWarps) {
+        send(at, bar, to, all);
+        if (RESETS && lane == 0) send(ptx::smem_u32(&ex->slot_reset[slot][rank]), bar, to, (int)reset);
+    }
+    if (threadIdx.x == 0)
+        ptx::mbar_arrive_expect_tx(&ex->met[slot], K * (32 * (int)sizeof(Run<V>) + (RESETS ? 4 : 0)));
+}
+// All ranks' runs of a step: the state in front of this rank's tile, and `run` behind all tiles.
+template <int V, int STAGES, bool RESETS>
+__device__ __forceinline__ Lane<V> meet(Exchange<V, STAGES> *ex, const Run<V> *slots, int step, int K, int rank,
+                                        Lane<V> &run, unsigned *err) {
+    const int lane = threadIdx.x & 31, slot = step % kSlots;
+    ptx::mbar_wait(&ex->met[slot], (step / kSlots) & 1, &ex->abort, err);
+    Lane<V> in = run;
+    for (int r = 0; r < K; ++r) {
+        if (r == rank) in = run;
+        const Run<V> e = slots[((size_t)slot * K + r) * 32 + lane];
+        run = (RESETS && ex->slot_reset[slot][r]) ? e.H : fma(e.P, run, e.H);
+    }
+    return in;
+}
+
+// A warp's rows in registers, from walk 1 to walk 2.
+template <typename IO, typename SH, bool PACKED>
+struct Rows {
+    Lane<SH::V> a[SH::S];
+    Raw<IO, SH::V> x[SH::S];
+    Run<SH::V> front;       // the rows of the tile in front of the warp's
+    Run<SH::V> tile;
+    bool front_reset, tile_reset;
+    // packed: the row code of row `lane`; bits of the rows that are a sequence's, its first, its last
+    int code;
+    uint32_t held, first, last;
+};
+
+template <typename IO, typename SH, int STAGES, bool BLEND, bool PACKED, bool AHEAD, bool TMA>
+__global__ void __launch_bounds__(kThreads, AHEAD ? 1 : 2) scan_kernel(const __grid_constant__ KernelParams q) {
+    static_assert(TMA || SH::V == 1, "copied rows have one channel a lane");
+    constexpr int V = SH::V, S = SH::S, CH = SH::CH, TT = SH::TT;
+    using L = Lane<V>;
+    using St = ScanStage<IO, SH, TMA>;
+    constexpr uint32_t kStage = St::bytes(PACKED);
+    extern __shared__ __align__(128) unsigned char ring[];
+    auto *ex = reinterpret_cast<Exchange<V, STAGES> *>(ring + (size_t)STAGES * kStage);
+    auto *slots = reinterpret_cast<Run<V> *>(ring + (size_t)STAGES * kStage + exchange_bytes<V, STAGES>());
+    const ScanParams &p = q.s;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int K = p.K, rank = blockIdx.x % K;
+    const long long col = blockIdx.x / K;
+    const int b = (int)(col / p.blocks);
+    const int cb = (int)(col % p.blocks) * CH, c0 = cb + lane * V;
+    const bool act = c0 < p.C;
+    const long long T = p.T, C = p.C;
+    start_exchange(ex, K, 2);
+    auto tile_row = [&](int step) { return ((long long)step * K + rank) * TT; };
+
+    // The first lanes of warps 0 and 4 ask for a step's gates and x (asking takes a lane some 200
+    // cycles for a box, and its warp with it).
+    const int asks = lane == 0 ? (warp == 0 ? 0 : warp == 4 ? 1 : -1) : -1;
+    const IO *xc = static_cast<const IO *>(p.x) + b * T * C + c0;
+    auto fetch = [&](int step) {
+        const long long t0 = tile_row(step);
+        if constexpr (!TMA) {
+            const long long w0 = t0 + warp * S;
+            if (step < p.steps && w0 < T) {
+                const int n = T - w0 < S ? (int)(T - w0) : S;
+                unsigned char *at = ring + (size_t)(step % STAGES) * kStage;
+                if (act) {
+                    const bool edge = (b == 0 && w0 == 0) || (b == p.B - 1 && w0 + S >= T);
+                    copy_rows<CH>(reinterpret_cast<uint32_t *>(at) + warp * S * CH + lane, p.gate + (b * T + w0) * C + c0, C, n, false);
+                    copy_rows<CH>(reinterpret_cast<uint32_t *>(at + St::kGate) + warp * S * CH + lane, xc + w0 * C, C, n, edge);
+                }
+                // codes exist in whole tiles, zeros behind the last row
+                if (PACKED && lane < S) copy_word(at + St::kGate + St::kX + (warp * S + lane) * 4, p.codes + w0 + lane);
+            }
+            copy_commit();
+            return;
+        }
+        if (asks < 0 || step >= p.steps || t0 >= T) return;
+        const uint32_t to = ptx::smem_u32(ring + (size_t)(step % STAGES) * kStage);
+        uint64_t *bar = &ex->full[step % STAGES];
+        if (asks == 0) {
+            ptx::mbar_arrive_expect_tx(bar, St::kGate);
+            ptx::tma_load_3d(to, &q.gate, cb, (int)t0, b, bar);
+        } else {
+            ptx::mbar_arrive_expect_tx(bar, St::kX + (PACKED ? TT * 4 : 0));
+            ptx::tma_load_3d(to + St::kGate, &q.x, cb, (int)t0, b, bar);
+            if (PACKED) ptx::bulk_load(to + St::kGate + St::kX, p.codes + t0, TT * 4, bar);
+        }
+    };
+    for (int i = 0; i < STAGES; ++i) fetch(i);
+
+    constexpr uint32_t kAllRows = S == 32 ? ~0u : (1u << S) - 1;
+    int stage = 0;
+    uint32_t parity = 0;
+    using R = Rows<IO, SH, PACKED>;
+    auto next_h = [&](const R &w, int s, L h) {
+        L u = BLEND ? blended(w.a[s], w.x[s].wide()) : w.x[s].wide();
+        if constexpr (PACKED) {   // at a first row a is its h
+            const bool first = w.first >> s & 1;
+            if (BLEND) u = pick(first, L::all(0.f), u);
+            h = pick(first, L::all(1.f), h);
+        }
+        return fma(w.a[s], h, u);
+    };
+    auto walk1 = [&](int step, R &w) {
+        const long long t0 = tile_row(step) + warp * S;
+        Run<V> own = Run<V>::none();
+        bool reset = false;
+        if constexpr (!TMA) copy_wait<STAGES - 1>();
+        if (TMA ? tile_row(step) < T : t0 < T) {
+            if constexpr (TMA) ptx::mbar_wait(&ex->full[stage], parity, &ex->abort, q.err);
+            unsigned char *at = ring + (size_t)stage * kStage;
+            float *sa = reinterpret_cast<float *>(at) + warp * S * CH + lane * V;
+            IO *sx = reinterpret_cast<IO *>(at + St::kGate) + warp * S * CH + lane * V;
+            uint32_t *sw = reinterpret_cast<uint32_t *>(at + St::kGate) + warp * S * CH + lane;   // copied words
+            auto take = [&](Raw<IO, V> &x, int s) {
+                if constexpr (TMA) x.load(sx + s * CH);
+                else pick_word(x, sw[s * CH], xc, (t0 + s) * C);
+            };
+            auto clear = [&](int s) {
+                if constexpr (TMA) L::all(0.f).store(sx + s * CH);
+                else sw[s * CH] = 0;
+            };
+            if constexpr (PACKED) {
+                // Rows of no sequence get a = 1, x = 0, which leaves the state.  A sequence's first
+                // row starts from its slot of the states, here and now (walk 2 comes when the slot
+                // may be overwritten): the row's h takes its gate's place, to be multiplied by 1.
+                // Done in the ring, row by row, so that the walks hold a choice at each row but no
+                // branch: branches (or a second copy of the walks) cost a warp more than the walk.
+                w.code = lane < S ? reinterpret_cast<const int *>(at + St::kGate + St::kX)[warp * S + lane] : 0;
+                w.held = __ballot_sync(~0u, w.code != 0);
+                w.first = __ballot_sync(~0u, row_first(w.code));
+                w.last = __ballot_sync(~0u, row_last(w.code));
+                reset = w.first != 0;
+                for (uint32_t m = ~w.held & kAllRows; m; m &= m - 1) {
+                    const int s = __ffs(m) - 1;
+                    L::all(1.f).store(sa + s * CH);
+                    clear(s);
+                }
+                for (uint32_t m = w.first; m; m &= m - 1) {
+                    const int s = __ffs(m) - 1;
+                    const long long seq = row_seq(__shfl_sync(~0u, w.code, s));
+                    Raw<IO, V> x;
+                    take(x, s);
+                    const L a = L::load(sa + s * CH);
+                    L h = BLEND ? blended(a, x.wide()) : x.wide();
+                    if (act && p.state_in) h = fma(a, L::load(p.state_in + seq * C + c0), h);
+                    h.store(sa + s * CH);
+                    clear(s);
+                }
+                if (TMA && (w.held != kAllRows || w.first)) ptx::fence_async_smem();   // before the ring's next copy
+            }
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                w.a[s] = L::load(sa + s * CH);
+                take(w.x[s], s);
+            }
+            if (!PACKED && t0 + S > T) {   // rows behind the end: a = 1, x = 0 leaves the state
+#pragma unroll
+                for (int s = 0; s < S; ++s)
+                    if (t0 + s >= T) w.a[s] = L::all(1.f), w.x[s].zero();
+            }
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                own.H = next_h(w, s, own.H);
+                own.P = mul(own.P, w.a[s]);
+            }
+        }
+        if (++stage == STAGES) stage = 0, parity ^= 1;
+        const int par = step & 1;
+        ex->warp[par][warp][lane] = own;
+        if (PACKED && lane == 0) ex->reset[par][warp] = reset;
+        __syncthreads();
+        fetch(step + STAGES);
+        w.front = w.tile = Run<V>::none();
+        w.front_reset = w.tile_reset = false;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+            if (i == warp) w.front = w.tile, w.front_reset = w.tile_reset;
+            const Run<V> r = ex->warp[par][i][lane];
+            if (PACKED && ex->reset[par][i]) {
+                w.tile = r, w.tile_reset = true;
+            } else {
+                w.tile.H = fma(r.P, w.tile.H, r.H);
+                w.tile.P = mul(w.tile.P, r.P);
+            }
+        }
+        if (K > 1) send_run<V, STAGES, PACKED>(ex, slots, step, K, rank, w.tile, w.tile_reset);
+    };
+
+    L run = L::all(0.f);
+    if (!PACKED && act && p.state_in) run = L::load(p.state_in + b * C + c0);
+    IO *hb = p.h ? static_cast<IO *>(p.h) + b * T * C + c0 : nullptr;
+    auto walk2 = [&](int step, R &w) {
+        L in = run;
+        if (K > 1) in = meet<V, STAGES, PACKED>(ex, slots, step, K, rank, run, q.err);
+        else run = (PACKED && w.tile_reset) ? w.tile.H : fma(w.tile.P, run, w.tile.H);
+        const long long t0 = tile_row(step) + warp * S;
+        if ((!PACKED && !act) || t0 >= T) return;
+        L h = (PACKED && w.front_reset) ? w.front.H : fma(w.front.P, in, w.front.H);
+        if (p.ckpt && t0 % kScanCheckpoint == 0) {
+            const long long rows = (T + kScanCheckpoint - 1) / kScanCheckpoint;
+            h.store(p.ckpt + (b * rows + t0 / kScanCheckpoint) * C + c0);
+        }
+        if (!hb) return;
+        IO *to = hb + t0 * C;
+        if constexpr (PACKED) {
+            // lanes without channels are still here, for the shuffles
+            const uint32_t stored = act ? w.held : 0;
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                w.a[s] = h = next_h(w, s, h);
+                if (stored >> s & 1) h.store(to);
+                to += C;
+            }
+            for (uint32_t m = w.last; m; m &= m - 1) {   // the last rows' h, to their sequences' states
+                const int last = __ffs(m) - 1;
+                const long long seq = row_seq(__shfl_sync(~0u, w.code, last));
+                L end = w.a[0];
+#pragma unroll
+                for (int s = 1; s < S; ++s) end = pick(s == last, w.a[s], end);
+                if (act) end.store(p.state_out + seq * C + c0);
+            }
+        } else if (t0 + S <= T) {
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                h = next_h(w, s, h);
+                h.store(to);
+                to += C;
+            }
+        } else {
+#pragma unroll 1
+            for (int n = 0; t0 + n < T; ++n) {
+                L a = w.a[0];
+                Raw<IO, V> x = w.x[0];
+#pragma unroll
+                for (int s = 1; s < S; ++s)
+                    if (s == n) a = w.a[s], x = w.x[s];
+                h = fma(a, h, BLEND ? blended(a, x.wide()) : x.wide());
+                h.store(to);
+                to += C;
+            }
+        }
+    };
+    R w;
+    if constexpr (AHEAD) {
+        walk1(0, w);
+        for (int step = 0; step < p.steps; ++step) {
+            R next;
+            if (step + 1 < p.steps) walk1(step + 1, next);
+            walk2(step, w);
+            w = next;
+        }
+    } else {
+        for (int step = 0; step < p.steps; ++step) {
+            walk1(step, w);
+            walk2(step, w);
+        }
+    }
+    if (!PACKED && rank == 0 && warp == 0 && act && p.state_out) run.store(p.state_out + b * C + c0);
+    if constexpr (!TMA) copy_wait<0>();
+    end_exchange(ex, K);
+}
+
+template <typename IO, typename SH>
+struct BackwardRows {
+    Lane<SH::V> a[SH::S];
+    Raw<IO, SH::V> x[SH::S], d[SH::S];
+    Lane<SH::V> front;            // forwards: the state in front of the warp's rows
+    Run<SH::V> behind, tile;      // backwards: the rows of the tile behind the warp's, and the tile
+};
+
+// Tiles from the last row to the first.  A run of rows acts on m (the next row's a l) as
+// m -> P m + M.  h_{t-1} comes from the checkpoint in front of every 32nd row.
+template <typename IO, typename SH, int STAGES, bool BLEND, bool AHEAD, bool TMA>
+__global__ void __launch_bounds__(kThreads, AHEAD ? 1 : 2)
+scan_backward_kernel(const __grid_constant__ BackwardKernelParams q) {
+    static_assert(TMA || SH::V == 1, "copied rows have one channel a lane");
+    constexpr int V = SH::V, S = SH::S, CH = SH::CH, TT = SH::TT;
+    constexpr int kGroups = kScanCheckpoint / S;   // warps between two checkpoints
+    static_assert(kScanCheckpoint % S == 0 && TT % kScanCheckpoint == 0, "tiles hold whole checkpoint spans");
+    using L = Lane<V>;
+    using St = BackwardStage<IO, SH, TMA>;
+    constexpr uint32_t kStage = St::bytes();
+    extern __shared__ __align__(128) unsigned char ring[];
+    auto *ex = reinterpret_cast<Exchange<V, STAGES> *>(ring + (size_t)STAGES * kStage);
+    auto *slots = reinterpret_cast<Run<V> *>(ring + (size_t)STAGES * kStage + exchange_bytes<V, STAGES>());
+    const BackwardParams &p = q.b;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int K = p.K, rank = blockIdx.x % K;
+    const long long col = blockIdx.x / K;
+    const int b = (int)(col / p.blocks);
+    const int cb = (int)(col % p.blocks) * CH, c0 = cb + lane * V;
+    const bool act = c0 < p.C;
+    const long long T = p.T, C = p.C;
+    const long long tiles = (T + TT - 1) / TT, rows = (T + kScanCheckpoint - 1) / kScanCheckpoint;
+    start_exchange(ex, K, 3);
+    // negative (before the first row) at the last steps of some ranks
+    auto tile_row = [&](int step) { return (tiles - 1 - ((long long)step * K + rank)) * TT; };
+
+    const uint32_t kept_bytes = (uint32_t)(C - cb < CH ? C - cb : CH) * sizeof(float);
+    // gates, x, and dh with the checkpoint rows: the first lanes of three warps
+    const int asks = lane == 0 ? (warp == 0 ? 0 : warp == 3 ? 1 : warp == 6 ? 2 : -1) : -1;
+    const IO *xc = static_cast<const IO *>(p.x) + b * T * C + c0, *dc = static_cast<const IO *>(p.dh) + b * T * C + c0;
+    const bool kept = warp % kGroups == 0;   // the warp's rows start at a checkpoint
+    auto fetch = [&](int step) {
+        const long long t0 = tile_row(step);
+        if constexpr (!TMA) {
+            const long long w0 = t0 + warp * S;
+            if (step < p.steps && w0 >= 0 && w0 < T && act) {
+                const int n = T - w0 < S ? (int)(T - w0) : S;
+                unsigned char *at = ring + (size_t)(step % STAGES) * kStage;
+                const int o = warp * S * CH + lane;
+                const bool edge = (b == 0 && w0 == 0) || (b == p.B - 1 && w0 + S >= T);
+                copy_rows<CH>(reinterpret_cast<uint32_t *>(at) + o, p.gate + (b * T + w0) * C + c0, C, n, false);
+                copy_rows<CH>(reinterpret_cast<uint32_t *>(at + St::kGate) + o, xc + w0 * C, C, n, edge);
+                copy_rows<CH>(reinterpret_cast<uint32_t *>(at + St::kGate + St::kX) + o, dc + w0 * C, C, n, edge);
+                if (kept)
+                    copy_word(at + St::kKept + (warp / kGroups * CH + lane) * 4, p.ckpt + (b * rows + w0 / kScanCheckpoint) * C + c0);
+            }
+            copy_commit();
+            return;
+        }
+        if (asks < 0 || step >= p.steps || t0 < 0) return;
+        const uint32_t to = ptx::smem_u32(ring + (size_t)(step % STAGES) * kStage);
+        uint64_t *bar = &ex->full[step % STAGES];
+        if (asks == 0) {
+            ptx::mbar_arrive_expect_tx(bar, St::kGate);
+            ptx::tma_load_3d(to, &q.gate, cb, (int)t0, b, bar);
+        } else if (asks == 1) {
+            ptx::mbar_arrive_expect_tx(bar, St::kX);
+            ptx::tma_load_3d(to + St::kGate, &q.x, cb, (int)t0, b, bar);
+        } else {
+            const long long k0 = t0 / kScanCheckpoint;
+            const int spans = rows - k0 < St::kSpans ? (int)(rows - k0) : St::kSpans;
+            ptx::mbar_arrive_expect_tx(bar, St::kX + spans * kept_bytes);
+            ptx::tma_load_3d(to + St::kGate + St::kX, &q.dh, cb, (int)t0, b, bar);
+            for (int i = 0; i < spans; ++i)
+                ptx::bulk_load(to + St::kKept + i * CH * (uint32_t)sizeof(float), p.ckpt + (b * rows + k0 + i) * C + cb,
+                               kept_bytes, bar);
+        }
+    };
+    for (int i = 0; i < STAGES; ++i) fetch(i);
+
+    int stage = 0;
+    uint32_t parity = 0;
+    using R = BackwardRows<IO, SH>;
+    auto walk1 = [&](int step, R &w) {
+        const long long t0 = tile_row(step) + warp * S;
+        Run<V> own = Run<V>::none();
+        L M = L::all(0.f), k = L::all(0.f);
+        if constexpr (!TMA) copy_wait<STAGES - 1>();
+        if (tile_row(step) >= 0) {
+            if constexpr (TMA) ptx::mbar_wait(&ex->full[stage], parity, &ex->abort, q.err);
+            const unsigned char *at = ring + (size_t)stage * kStage;
+            const int o = warp * S * CH + lane * V;
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                w.a[s] = L::load(reinterpret_cast<const float *>(at) + o + s * CH);
+                if constexpr (TMA) {
+                    w.x[s].load(reinterpret_cast<const IO *>(at + St::kGate) + o + s * CH);
+                    w.d[s].load(reinterpret_cast<const IO *>(at + St::kGate + St::kX) + o + s * CH);
+                } else {
+                    pick_word(w.x[s], reinterpret_cast<const uint32_t *>(at + St::kGate)[o + s * CH], xc, (t0 + s) * C);
+                    pick_word(w.d[s], reinterpret_cast<const uint32_t *>(at + St::kGate + St::kX)[o + s * CH], dc, (t0 + s) * C);
+                }
+            }
+            if (kept && act && t0 < T)
+                k = L::load(reinterpret_cast<const float *>(at + St::kKept) + warp / kGroups * CH + lane * V);
+            if (t0 + S > T) {
+#pragma unroll
+                for (int s = 0; s < S; ++s)
+                    if (t0 + s >= T) w.a[s] = L::all(1.f), w.x[s].zero(), w.d[s].zero();
+            }
+            // P and H forwards (H from the checkpoint where the warp has one); M is the sum over
+            // the rows of dh times the product of the gates up to the row
+            own.H = k;
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                own.H = fma(w.a[s], own.H, BLEND ? blended(w.a[s], w.x[s].wide()) : w.x[s].wide());
+                own.P = mul(own.P, w.a[s]);
+                M = fma(own.P, w.d[s].wide(), M);
+            }
+        }
+        if (++stage == STAGES) stage = 0, parity ^= 1;
+        const int par = step & 1;
+        ex->warp[par][warp][lane] = own;
+        ex->back[par][warp][lane] = M;
+        __syncthreads();
+        fetch(step + STAGES);
+        w.front = k;
+        if (!kept) {
+            const int from = warp / kGroups * kGroups;
+            w.front = ex->warp[par][from][lane].H;
+            for (int i = from + 1; i < warp; ++i) {
+                const Run<V> r = ex->warp[par][i][lane];
+                w.front = fma(r.P, w.front, r.H);
+            }
+        }
+        w.behind = w.tile = Run<V>::none();
+#pragma unroll
+        for (int i = kWarps - 1; i >= 0; --i) {
+            if (i == warp) w.behind = w.tile;
+            const L P = ex->warp[par][i][lane].P;
+            w.tile.H = fma(P, w.tile.H, ex->back[par][i][lane]);
+            w.tile.P = mul(w.tile.P, P);
+        }
+        if (K > 1) send_run<V, STAGES, false>(ex, slots, step, K, rank, w.tile, false);
+    };
+
+    L run = L::all(0.f);
+    if (act && p.dstate) run = L::load(p.dstate + b * C + c0);
+    IO *ob = static_cast<IO *>(p.dx) + b * T * C + c0;
+    float *gb = p.dgate ? p.dgate + b * T * C + c0 : nullptr;
+    auto walk2 = [&](int step, R &w) {
+        L in = run;
+        if (K > 1) in = meet<V, STAGES, false>(ex, slots, step, K, rank, run, q.err);
+        else run = fma(w.tile.P, run, w.tile.H);
+        const long long t0 = tile_row(step) + warp * S;
+        if (!act || t0 < 0 || t0 >= T) return;
+        L before[S], h = w.front, m = fma(w.behind.P, in, w.behind.H);
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            before[s] = h;
+            h = fma(w.a[s], h, BLEND ? blended(w.a[s], w.x[s].wide()) : w.x[s].wide());
+        }
+        auto row = [&](int s, IO *to, float *tg) {
+            const L l = add(w.d[s].wide(), m);
+            m = mul(w.a[s], l);
+            (BLEND ? blended(w.a[s], l) : l).store(to);
+            if (tg) mul(l, BLEND ? sub(before[s], w.x[s].wide()) : before[s]).store(tg);
+        };
+        IO *to = ob + (t0 + S - 1) * C;
+        if (t0 + S <= T && gb) {
+            float *tg = gb + (t0 + S - 1) * C;
+#pragma unroll
+            for (int s = S - 1; s >= 0; --s) {
+                row(s, to, tg);
+                to -= C;
+                tg -= C;
+            }
+        } else {
+#pragma unroll
+            for (int s = S - 1; s >= 0; --s)
+                if (t0 + s < T) row(s, ob + (t0 + s) * C, gb ? gb + (t0 + s) * C : nullptr);
+        }
+    };
+    R w;
+    if constexpr (AHEAD) {
+        walk1(0, w);
+        for (int step = 0; step < p.steps; ++step) {
+            R next;
+            if (step + 1 < p.steps) walk1(step + 1, next);
+            walk2(step, w);
+            w = next;
+        }
+    } else {
+        for (int step = 0; step < p.steps; ++step) {
+            walk1(step, w);
+            walk2(step, w);
+        }
+    }
+    if (rank == 0 && warp == 0 && act && p.dstate0) run.store(p.dstate0 + b * C + c0);
+    if constexpr (!TMA) copy_wait<0>();
+    end_exchange(ex, K);
 }
 
 // One token: no reuse, every operand once.  Flat over N * C elements, V a thread (the last ones
@@ -678,36 +835,6 @@ scan_rows_kernel(int T, int padded, int row_blocks, int N, long long C, const in
 
 // ------------------------------------------------------------------------------- host side
 
-template <typename IO, typename SH, int STAGES, bool BLEND, bool PACKED>
-struct Forward {
-    static constexpr auto kernel = scan_kernel<IO, SH, STAGES, BLEND, PACKED>;
-    static constexpr int kBlock = kThreads, kChannels = SH::CH, kMost = 16;
-    static constexpr double kRate = 4000.0;
-    static constexpr double kTileBytes = (double)kThreads * SH::E * (sizeof(float) + 2 * sizeof(IO));
-    static double step_ns(int K) { return 2200.0 + (K > 1 ? 300.0 : 0.0); }
-    static size_t smem(int K) { return scan_ring_bytes<IO, SH, STAGES>() + exchange_bytes<SH>(K); }
-    static long long cols(const ScanArgs &a) { return (long long)a.B * ((a.C + SH::CH - 1) / SH::CH); }
-    static long long tiles(const ScanArgs &a) { return ((long long)a.T + SH::TT - 1) / SH::TT; }
-    static cudaError_t launch(const ScanArgs &a, int K) {
-        return launch_cluster<Forward>(scan_params<Forward>(a, K), cols(a), K, a.stream);
-    }
-};
-
-template <typename IO, typename SH, int STAGES, bool BLEND>
-struct Backward {
-    static constexpr auto kernel = scan_backward_kernel<IO, SH, STAGES, BLEND>;
-    static constexpr int kBlock = kThreads, kChannels = SH::CH, kMost = 16;
-    static constexpr double kRate = 4000.0;
-    static constexpr double kTileBytes = (double)kThreads * SH::E * (2 * sizeof(float) + 3 * sizeof(IO));
-    static double step_ns(int K) { return 2200.0 + (K > 1 ? 300.0 : 0.0); }
-    static size_t smem(int K) { return backward_ring_bytes<IO, SH, STAGES>() + exchange_bytes<SH>(K); }
-    static long long cols(const ScanBackwardArgs &a) { return (long long)a.B * ((a.C + SH::CH - 1) / SH::CH); }
-    static long long tiles(const ScanBackwardArgs &a) { return ((long long)a.T + SH::TT - 1) / SH::TT; }
-    static cudaError_t launch(const ScanBackwardArgs &a, int K) {
-        return launch_cluster<Backward>(backward_params<Backward>(a, K), cols(a), K, a.stream);
-    }
-};
-
 // Channels a thread: the widest vectors that the rows' length and the tensors' starts allow.
 template <typename IO>
 int vector_width(long long C, std::initializer_list<const void *> io, std::initializer_list<const void *> fp32) {
@@ -720,34 +847,137 @@ int vector_width(long long C, std::initializer_list<const void *> io, std::initi
     return 1;
 }
 
-template <typename IO, int V, bool BLEND, bool PACKED>
-cudaError_t forward_v(const ScanArgs &a) {
-    constexpr int E = sizeof(IO) == 2 && V > 1 ? 32 : 16, STAGES = sizeof(IO) == 2 ? 2 : 3;
-    return launch_best<Forward<IO, Shape<V, 16, E>, STAGES, BLEND, PACKED>,
-                       Forward<IO, Shape<V, 4, E>, STAGES, BLEND, PACKED>>(a);
+
+// Row tensors as TMA sees them: [B][T][C] in boxes of TT rows x CH channels.
+template <typename SH, typename IO>
+bool row_map(CUtensorMap *map, const IO *base, long long B, long long T, long long C) {
+    return make_tmap_3d(map, base, sizeof(IO) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                        sizeof(IO), C, T, B, C * sizeof(IO), T * C * sizeof(IO), SH::CH, SH::TT, false);
 }
-template <typename IO, int V>
-cudaError_t forward_flags(const ScanArgs &a) {
-    if (a.codes) return a.blend ? forward_v<IO, V, true, true>(a) : forward_v<IO, V, false, true>(a);
-    return a.blend ? forward_v<IO, V, true, false>(a) : forward_v<IO, V, false, false>(a);
+
+// BASE and MORE: ns of a CTA's step alone on its SM, and more for each doubling of K (measured:
+// (time of a call with few columns - 6 us) / steps).  RATE: bytes a ns of all CTAs together
+// (measured where the columns fill the SMs).
+template <typename IO, typename SH, int STAGES, bool BLEND, bool PACKED, bool AHEAD, int MOST, int BASE, int MORE, int RATE,
+          bool TMA = true>
+struct Forward {
+    static constexpr auto kernel = scan_kernel<IO, SH, STAGES, BLEND, PACKED, AHEAD, TMA>;
+    static constexpr int kBlock = kThreads, kChannels = SH::CH, kMost = MOST;
+    static constexpr double kTileBytes = (double)SH::TT * SH::CH * (sizeof(float) + 2 * sizeof(IO));
+    static constexpr double kRate = RATE;
+    static double step_ns(int K) { return BASE + MORE * std::log2((double)K); }
+    static size_t smem(int K) {
+        return (size_t)STAGES * ScanStage<IO, SH, TMA>::bytes(PACKED) + exchange_bytes<SH::V, STAGES>() +
+               (K > 1 ? (size_t)kSlots * K * 32 * sizeof(Run<SH::V>) : 0);
+    }
+    static long long cols(const ScanArgs &a) { return (long long)a.B * ((a.C + SH::CH - 1) / SH::CH); }
+    static long long tiles(const ScanArgs &a) { return ((long long)a.T + SH::TT - 1) / SH::TT; }
+    static cudaError_t launch(const ScanArgs &a, int K) {
+        KernelParams q;
+        if (TMA && (!row_map<SH>(&q.gate, a.gate, a.B, a.T, a.C) ||
+                    !row_map<SH>(&q.x, static_cast<const IO *>(a.x), a.B, a.T, a.C)))
+            return cudaErrorInvalidValue;
+        q.s = scan_params<Forward>(a, K);
+        q.err = device_error_word();
+        return launch_cluster<Forward>(q, cols(a), K, a.stream);
+    }
+};
+
+template <typename IO, typename SH, int STAGES, bool BLEND, bool AHEAD, int MOST, int BASE, int MORE, int RATE,
+          bool TMA = true>
+struct Backward {
+    static constexpr auto kernel = scan_backward_kernel<IO, SH, STAGES, BLEND, AHEAD, TMA>;
+    static constexpr int kBlock = kThreads, kChannels = SH::CH, kMost = MOST;
+    static constexpr double kTileBytes = (double)SH::TT * SH::CH * (2 * sizeof(float) + 3 * sizeof(IO));
+    static constexpr double kRate = RATE;
+    static double step_ns(int K) { return BASE + MORE * std::log2((double)K); }
+    static size_t smem(int K) {
+        return (size_t)STAGES * BackwardStage<IO, SH, TMA>::bytes() + exchange_bytes<SH::V, STAGES>() +
+               (K > 1 ? (size_t)kSlots * K * 32 * sizeof(Run<SH::V>) : 0);
+    }
+    static long long cols(const ScanBackwardArgs &a) { return (long long)a.B * ((a.C + SH::CH - 1) / SH::CH); }
+    static long long tiles(const ScanBackwardArgs &a) { return ((long long)a.T + SH::TT - 1) / SH::TT; }
+    static cudaError_t launch(const ScanBackwardArgs &a, int K) {
+        BackwardKernelParams q;
+        if (TMA && (!row_map<SH>(&q.gate, a.gate, a.B, a.T, a.C) ||
+                    !row_map<SH>(&q.x, static_cast<const IO *>(a.x), a.B, a.T, a.C) ||
+                    !row_map<SH>(&q.dh, static_cast<const IO *>(a.dh), a.B, a.T, a.C)))
+            return cudaErrorInvalidValue;
+        q.b = backward_params<Backward>(a, K);
+        q.err = device_error_word();
+        return launch_cluster<Backward>(q, cols(a), K, a.stream);
+    }
+};
+
+// Rows and starts on 16 bytes (a lane's vectors and the checkpoints' copies divide them), outputs
+// on the vectors of a lane, sizes within a tensor map.
+bool rows_fit(long long T, long long C, size_t elem, std::initializer_list<const void *> in,
+              std::initializer_list<const void *> out) {
+    if (C * elem % 16 || C * 4 % 16 || T * C * 4 >= (1ll << 40)) return false;
+    for (const void *q : in)
+        if (reinterpret_cast<uintptr_t>(q) % 16) return false;
+    for (const void *q : out)
+        if (reinterpret_cast<uintptr_t>(q) % 8) return false;
+    return true;
+}
+
+bool rows_by_tma(const ScanArgs &a) {
+    return rows_fit(a.T, a.C, a.dtype == LA_BF16 ? 2 : 4, {a.x, a.gate}, {a.h, a.ckpt, a.state_in, a.state_out});
+}
+bool rows_by_tma(const ScanBackwardArgs &a) {
+    return rows_fit(a.T, a.C, a.dtype == LA_BF16 ? 2 : 4, {a.x, a.gate, a.dh, a.ckpt},
+                    {a.dx, a.dgate, a.dstate, a.dstate0});
+}
+
+// The variants, of which a call takes the one with the least estimated time:
+//   two CTAs an SM, K = 1, a step after the other: many columns;
+//   one CTA an SM, AHEAD, K = 1 .. 16: few columns, and with a ring of 144 KB and more also the
+//   fastest where 32-channel columns fill the SMs once (B2 T32768 C2048 bf16: 167 us against 172).
+// V = 2 has half the columns and 256-byte gate rows, V = 1 twice the CTAs.
+// Rows that TMA cannot take are bound by their lanes' copies (two a value, 4 bytes each): B2
+// T5000 C1001 bf16 38 us, floor 12.
+template <typename IO, bool BLEND, bool PACKED>
+cudaError_t forward(const ScanArgs &a) {
+    if (!rows_by_tma(a))
+        return launch_best<Forward<IO, Shape<1, 16>, 3, BLEND, PACKED, false, 4, 1500, 150, 3200, false>,
+                           Forward<IO, Shape<1, 32>, 3, BLEND, PACKED, true, 16, 2350, 150, 2600, false>>(a);
+    if constexpr (sizeof(IO) == 2)
+        return launch_best<Forward<IO, Shape<2, 32>, 2, BLEND, PACKED, false, 1, 900, 0, 6400>,
+                           Forward<IO, Shape<1, 32>, 2, BLEND, PACKED, false, 1, 1200, 0, 6300>,
+                           Forward<IO, Shape<2, 32>, 3, BLEND, PACKED, true, 8, 1250, 50, 6300>,
+                           Forward<IO, Shape<1, 32>, 3, BLEND, PACKED, true, 16, 1250, 200, 6500>>(a);
+    else
+        return launch_best<Forward<IO, Shape<2, 16>, 3, BLEND, PACKED, false, 1, 670, 0, 6400>,
+                           Forward<IO, Shape<1, 16>, 3, BLEND, PACKED, false, 1, 680, 0, 6300>,
+                           Forward<IO, Shape<2, 32>, 3, BLEND, PACKED, true, 8, 1400, 60, 6200>,
+                           Forward<IO, Shape<1, 32>, 3, BLEND, PACKED, true, 16, 1450, 140, 6300>>(a);
 }
 template <typename IO>
 cudaError_t forward_io(const ScanArgs &a) {
-    const int V = vector_width<IO>(a.C, {a.x, a.h}, {a.gate, a.ckpt});
-    return V == 4 ? forward_flags<IO, 4>(a) : V == 2 ? forward_flags<IO, 2>(a) : forward_flags<IO, 1>(a);
+    if (a.codes) return a.blend ? forward<IO, true, true>(a) : forward<IO, false, true>(a);
+    return a.blend ? forward<IO, true, false>(a) : forward<IO, false, false>(a);
 }
 
-template <typename IO, int V, bool BLEND>
-cudaError_t backward_v(const ScanBackwardArgs &a) {
-    constexpr int E = sizeof(IO) == 2 && V > 1 ? 16 : 8, STAGES = sizeof(IO) == 2 ? 2 : 3;
-    return launch_best<Backward<IO, Shape<V, 16, E>, STAGES, BLEND>, Backward<IO, Shape<V, 4, E>, STAGES, BLEND>>(a);
+// The backward pass fills HBM best with two CTAs an SM and one step after the other (B2 T32768
+// C2048 bf16, K = 2: 329 us; one CTA an SM and AHEAD: 380 to 410, with more spread, although each
+// of its CTAs is faster alone), and has few columns go AHEAD.
+template <typename IO, bool BLEND>
+cudaError_t backward(const ScanBackwardArgs &a) {
+    if (!rows_by_tma(a))
+        return launch_best<Backward<IO, Shape<1, 8>, 3, BLEND, false, 4, 1650, 150, 3000, false>,
+                           Backward<IO, Shape<1, 16>, 4, BLEND, true, 16, 2600, 130, 2100, false>>(a);
+    if constexpr (sizeof(IO) == 2)
+        return launch_best<Backward<IO, Shape<2, 16>, 3, BLEND, false, 4, 1130, 150, 5900>,
+                           Backward<IO, Shape<2, 32>, 3, BLEND, true, 8, 1930, 30, 5000>,
+                           Backward<IO, Shape<1, 32>, 3, BLEND, true, 16, 2100, 250, 4600>>(a);
+    else
+        return launch_best<Backward<IO, Shape<2, 16>, 2, BLEND, false, 4, 1180, 150, 6000>,
+                           Backward<IO, Shape<2, 16>, 4, BLEND, true, 8, 1300, 60, 5300>,
+                           Backward<IO, Shape<1, 16>, 4, BLEND, true, 16, 1300, 100, 4800>>(a);
 }
 template <typename IO>
 cudaError_t backward_io(const ScanBackwardArgs &a) {
-    const int V = vector_width<IO>(a.C, {a.x, a.dh, a.dx}, {a.gate, a.ckpt, a.dgate});
-    if (V == 4) return a.blend ? backward_v<IO, 4, true>(a) : backward_v<IO, 4, false>(a);
-    if (V == 2) return a.blend ? backward_v<IO, 2, true>(a) : backward_v<IO, 2, false>(a);
-    return a.blend ? backward_v<IO, 1, true>(a) : backward_v<IO, 1, false>(a);
+    return a.blend ? backward<IO, true>(a) : backward<IO, false>(a);
 }
 
 }  // namespace
@@ -767,12 +997,9 @@ cudaError_t launch_scan_rows(const ScanArgs &a, const int *cu, int N, int *codes
 }
 
 cudaError_t launch_scan(const ScanArgs &a) {
-    if (scan_tma_takes(a)) return launch_scan_tma(a);
     return a.dtype == LA_BF16 ? forward_io<__nv_bfloat16>(a) : forward_io<float>(a);
 }
-
 cudaError_t launch_scan_backward(const ScanBackwardArgs &a) {
-    if (scan_tma_takes(a)) return launch_scan_backward_tma(a);
     return a.dtype == LA_BF16 ? backward_io<__nv_bfloat16>(a) : backward_io<float>(a);
 }
 

@@ -1,5 +1,5 @@
-// scan_util.cuh -- what the two forms of the gated linear recurrence share: row codes of packed
-// batches, the exchange through distributed shared memory, and the choice of the cluster width.
+// scan_util.cuh -- row codes of packed batches, parameters, and the choice of a variant and a cluster
+// width for the gated linear recurrence (scan.cu).
 #pragma once
 
 #include "la_internal.cuh"
@@ -27,6 +27,7 @@ struct ScanParams {
     float *ckpt;             // [B, ceil(T / 32), C]; nullptr: not kept
     const int *codes;        // packed: [T rounded up to kCodeRows]
     long long T, C;
+    int B;
     int blocks;              // channel blocks of one batch row
     int K;                   // CTAs of a cluster
     int steps;               // tiles each CTA walks
@@ -38,7 +39,7 @@ struct BackwardParams {
     void *dx;
     float *dgate, *dstate0;              // dstate0: nullptr: not kept
     long long T, C;
-    int blocks, K, steps;
+    int B, blocks, K, steps;
 };
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
@@ -151,7 +152,7 @@ ScanParams scan_params(const ScanArgs &a, int K) {
     p.x = a.x; p.gate = a.gate;
     p.state_in = a.state_in; p.state_out = a.state_out;
     p.h = a.h; p.ckpt = a.ckpt; p.codes = a.codes;
-    p.T = a.T; p.C = a.C;
+    p.T = a.T; p.C = a.C; p.B = a.B;
     p.blocks = (int)((a.C + L::kChannels - 1) / L::kChannels);
     p.K = K;
     p.steps = (int)((L::tiles(a) + K - 1) / K);
@@ -163,7 +164,7 @@ BackwardParams backward_params(const ScanBackwardArgs &a, int K) {
     p.x = a.x; p.dh = a.dh;
     p.gate = a.gate; p.ckpt = a.ckpt; p.dstate = a.dstate;
     p.dx = a.dx; p.dgate = a.dgate; p.dstate0 = a.dstate0;
-    p.T = a.T; p.C = a.C;
+    p.T = a.T; p.C = a.C; p.B = a.B;
     p.blocks = (int)((a.C + L::kChannels - 1) / L::kChannels);
     p.K = K;
     p.steps = (int)((L::tiles(a) + K - 1) / K);
