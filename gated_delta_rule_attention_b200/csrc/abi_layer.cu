@@ -1,0 +1,324 @@
+// abi_layer.cu -- the extern "C" entry points of the operators around the attention (declared in
+// include/la.h): the gated linear recurrence, rotary positions, the RMS norm.
+//
+// Host-side only, as abi.cu: argument checks, then a launcher on the caller's stream.  No entry
+// point allocates device memory or keeps a pointer past its return.
+#include "layer.h"
+
+#include <cstdint>
+
+namespace la {
+namespace {
+
+constexpr long long kMaxElems = 1ll << 40;
+
+// True if `p` is aligned memory that the current device can address as its own.
+bool tensor_ok(const void *p, uintptr_t align) {
+    if (!p || reinterpret_cast<uintptr_t>(p) % align) return false;
+    cudaPointerAttributes attr;
+    if (cudaPointerGetAttributes(&attr, p) != cudaSuccess) {
+        (void)cudaGetLastError();   // clear the non-sticky error this query may leave
+        return false;
+    }
+    if (attr.type == cudaMemoryTypeManaged) return true;
+    int dev = -1;
+    return attr.type == cudaMemoryTypeDevice && cudaGetDevice(&dev) == cudaSuccess && attr.device == dev;
+}
+
+la_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? LA_OK : LA_ERR_CUDA; }
+
+}  // namespace
+}  // namespace la
+
+using namespace la;
+
+// ---------------------------------------------------------------- gated linear recurrence
+
+namespace {
+
+// Checks shared by the dense forms: dtype, flags, sizes.
+bool scan_sizes_ok(int dtype, int B, int T, int C, unsigned flags, unsigned allowed) {
+    if (dtype != LA_F32 && dtype != LA_BF16) return false;
+    if (flags & ~allowed) return false;
+    return B >= 1 && T >= 0 && C >= 1 && (long long)B * C <= kMaxElems && (long long)B * T <= kMaxElems / C;
+}
+// Element alignment is enough: the kernels take narrower vectors where a tensor's start asks for it.
+bool scan_io_ok(int dtype, const void *p) { return tensor_ok(p, dtype == LA_BF16 ? 2 : 4); }
+size_t checkpoint_bytes(int B, int T, int C) {
+    return sizeof(float) * (size_t)B * (((size_t)T + kScanCheckpoint - 1) / kScanCheckpoint) * C;
+}
+
+}  // namespace
+
+extern "C" la_status_t la_linear_scan(la_dtype_t dtype, int B, int T, int C, const void *x, const float *gate,
+                                      float *state, void *h, float *checkpoints, unsigned flags, void *stream) {
+    timer_reset();
+    if (!scan_sizes_ok(dtype, B, T, C, flags, LA_FLAG_INIT_STATE | LA_SCAN_BLEND)) return LA_ERR_INVALID_ARG;
+    if (!tensor_ok(state, 4)) return LA_ERR_INVALID_ARG;
+    const bool init = (flags & LA_FLAG_INIT_STATE) != 0;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const size_t sb = sizeof(float) * (size_t)B * C;
+    if (T == 0) return init ? LA_OK : from_cuda(cudaMemsetAsync(state, 0, sb, st));
+    if (!scan_io_ok(dtype, x) || !tensor_ok(gate, 4) || !scan_io_ok(dtype, h) ||
+        (checkpoints && !tensor_ok(checkpoints, 4)))
+        return LA_ERR_INVALID_ARG;
+    const size_t n = (size_t)B * T * C, io = n * (dtype == LA_BF16 ? 2 : 4);
+    if (!writes_disjoint({{h, io}, {state, sb}, {checkpoints, checkpoint_bytes(B, T, C)}},
+                         {{x, io}, {gate, sizeof(float) * n}}))
+        return LA_ERR_INVALID_ARG;
+    ScanArgs a;
+    a.dtype = dtype;
+    a.B = B; a.T = T; a.C = C;
+    a.x = x; a.gate = gate;
+    a.state_in = init ? state : nullptr;
+    a.state_out = state;
+    a.h = h;
+    a.ckpt = checkpoints;
+    a.blend = (flags & LA_SCAN_BLEND) != 0;
+    a.stream = st;
+    return from_cuda(launch_scan(a));
+}
+
+extern "C" size_t la_linear_scan_varlen_workspace_size(int T) { return T < 1 ? 0 : scan_codes_bytes(T); }
+
+extern "C" la_status_t la_linear_scan_varlen(la_dtype_t dtype, int N, int T, int C, const int *cu_seqlens,
+                                             const void *x, const float *gate, float *state, void *h,
+                                             unsigned flags, void *workspace, size_t workspace_bytes, void *stream) {
+    timer_reset();
+    // a row's sequence number shares a 32-bit code with two flags; the codes are padded rows
+    if (N < 1 || N >= (1 << 29) || T > INT32_MAX - 512) return LA_ERR_INVALID_ARG;
+    if (!scan_sizes_ok(dtype, 1, T, C, flags, LA_FLAG_INIT_STATE | LA_SCAN_BLEND) || (long long)N > kMaxElems / C)
+        return LA_ERR_INVALID_ARG;
+    if (!tensor_ok(cu_seqlens, 4) || !tensor_ok(state, 4)) return LA_ERR_INVALID_ARG;
+    const size_t n = (size_t)T * C, io = n * (dtype == LA_BF16 ? 2 : 4);
+    if (T > 0) {
+        if (!scan_io_ok(dtype, x) || !tensor_ok(gate, 4) || !scan_io_ok(dtype, h) || !tensor_ok(workspace, 16) ||
+            workspace_bytes < la_linear_scan_varlen_workspace_size(T))
+            return LA_ERR_INVALID_ARG;
+    }
+    if (!writes_disjoint({{T > 0 ? h : nullptr, io}, {state, sizeof(float) * (size_t)N * C},
+                          {T > 0 ? workspace : nullptr, workspace_bytes}},
+                         {{cu_seqlens, sizeof(int) * ((size_t)N + 1)}, {T > 0 ? x : nullptr, io},
+                          {T > 0 ? gate : nullptr, sizeof(float) * n}}))
+        return LA_ERR_INVALID_ARG;
+    const bool init = (flags & LA_FLAG_INIT_STATE) != 0;
+    ScanArgs a;
+    a.dtype = dtype;
+    a.B = 1; a.T = T; a.C = C;
+    a.x = x; a.gate = gate;
+    a.state_in = init ? state : nullptr;
+    a.state_out = state;
+    a.h = h;
+    a.ckpt = nullptr;
+    a.blend = (flags & LA_SCAN_BLEND) != 0;
+    a.stream = static_cast<cudaStream_t>(stream);
+    int *codes = static_cast<int *>(workspace);
+    cudaError_t e = launch_scan_rows(a, cu_seqlens, N, codes, init ? nullptr : state);
+    if (e != cudaSuccess || T == 0) return from_cuda(e);
+    a.codes = codes;
+    return from_cuda(launch_scan(a));
+}
+
+extern "C" la_status_t la_linear_scan_step(la_dtype_t dtype, int N, int C, const void *x, const float *gate,
+                                           float *state, void *h, unsigned flags, void *stream) {
+    timer_reset();
+    if (!scan_sizes_ok(dtype, N, 1, C, flags, LA_SCAN_BLEND)) return LA_ERR_INVALID_ARG;
+    if (!scan_io_ok(dtype, x) || !tensor_ok(gate, 4) || !tensor_ok(state, 4) || !scan_io_ok(dtype, h))
+        return LA_ERR_INVALID_ARG;
+    const size_t n = (size_t)N * C, io = n * (dtype == LA_BF16 ? 2 : 4);
+    if (!writes_disjoint({{h, io}, {state, sizeof(float) * n}}, {{x, io}, {gate, sizeof(float) * n}}))
+        return LA_ERR_INVALID_ARG;
+    ScanArgs a;
+    a.dtype = dtype;
+    a.B = N; a.T = 1; a.C = C;
+    a.x = x; a.gate = gate;
+    a.state_in = a.state_out = state;
+    a.h = h;
+    a.ckpt = nullptr;
+    a.blend = (flags & LA_SCAN_BLEND) != 0;
+    a.stream = static_cast<cudaStream_t>(stream);
+    return from_cuda(launch_scan_step(a));
+}
+
+extern "C" size_t la_linear_scan_backward_workspace_size(int B, int T, int C) {
+    return B < 1 || T < 1 || C < 1 ? 0 : checkpoint_bytes(B, T, C);
+}
+
+extern "C" la_status_t la_linear_scan_backward(la_dtype_t dtype, int B, int T, int C, const void *x,
+                                               const float *gate, const float *state0,
+                                               const float *checkpoints, const void *dh, const float *dstate,
+                                               void *dx, float *dgate, float *dstate0, unsigned flags,
+                                               void *workspace, size_t workspace_bytes, void *stream) {
+    timer_reset();
+    if (!scan_sizes_ok(dtype, B, T, C, flags, LA_SCAN_BLEND) || T < 1) return LA_ERR_INVALID_ARG;
+    const void *need[] = {x, dh, dx};
+    for (const void *q : need)
+        if (!scan_io_ok(dtype, q)) return LA_ERR_INVALID_ARG;
+    if (!tensor_ok(gate, 4) || !(checkpoints ? tensor_ok(checkpoints, 4) : tensor_ok(workspace, 16)))
+        return LA_ERR_INVALID_ARG;
+    const float *may[] = {checkpoints ? nullptr : state0, dstate, dgate, dstate0};
+    for (const float *q : may)
+        if (q && !tensor_ok(q, 4)) return LA_ERR_INVALID_ARG;
+    const size_t n = (size_t)B * T * C, io = n * (dtype == LA_BF16 ? 2 : 4), sb = sizeof(float) * (size_t)B * C;
+    const size_t kb = checkpoint_bytes(B, T, C);
+    if (!checkpoints && workspace_bytes < kb) return LA_ERR_INVALID_ARG;
+    if (!writes_disjoint({{dx, io}, {dgate, sizeof(float) * n}, {dstate0, sb},
+                          {checkpoints ? nullptr : workspace, workspace_bytes}},
+                         {{x, io}, {gate, sizeof(float) * n}, {dh, io}, {dstate, sb}, {checkpoints, kb},
+                          {checkpoints ? nullptr : state0, sb}}))
+        return LA_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool blend = (flags & LA_SCAN_BLEND) != 0;
+    if (!checkpoints) {   // the forward walk once more, for the kept states alone
+        ScanArgs f;
+        f.dtype = dtype;
+        f.B = B; f.T = T; f.C = C;
+        f.x = x; f.gate = gate;
+        f.state_in = state0;
+        f.state_out = nullptr;
+        f.h = nullptr;
+        f.ckpt = static_cast<float *>(workspace);
+        f.blend = blend;
+        f.stream = st;
+        const cudaError_t e = launch_scan(f);
+        if (e != cudaSuccess) return from_cuda(e);
+        checkpoints = f.ckpt;
+    }
+    ScanBackwardArgs a;
+    a.dtype = dtype;
+    a.B = B; a.T = T; a.C = C;
+    a.x = x; a.dh = dh;
+    a.gate = gate; a.ckpt = checkpoints; a.dstate = dstate;
+    a.dx = dx; a.dgate = dgate; a.dstate0 = dstate0;
+    a.blend = blend;
+    a.stream = st;
+    return from_cuda(launch_scan_backward(a));
+}
+
+// ---------------------------------------------------------------- rotary positions
+
+extern "C" la_status_t la_rotary(la_dtype_t dtype, int B, int T, int H_q, int H_k, int d, int rotary_dim,
+                                 const void *q, const void *k, const double *freqs, const int *positions,
+                                 int start, float scale, void *y_q, void *y_k, unsigned flags, void *stream) {
+    timer_reset();
+    if (dtype != LA_F32 && dtype != LA_BF16) return LA_ERR_INVALID_ARG;
+    if (flags & ~(LA_ROT_INTERLEAVED | LA_ROT_TRANSPOSE | LA_ROT_X_TOKENS | LA_ROT_Y_TOKENS)) return LA_ERR_INVALID_ARG;
+    if (B < 1 || T < 0 || H_q < 1 || H_k < 0 || rotary_dim < 2 || rotary_dim % 2 || rotary_dim > d)
+        return LA_ERR_INVALID_ARG;
+    if (d > 512) return LA_ERR_UNSUPPORTED;
+    const long long most = H_q > H_k ? H_q : H_k;
+    if ((long long)B * T > kMaxElems / (most * d)) return LA_ERR_INVALID_ARG;
+    if (T == 0) return LA_OK;
+    if (!tensor_ok(freqs, 8) || (positions && !tensor_ok(positions, 4))) return LA_ERR_INVALID_ARG;
+    if (!tensor_ok(q, 16) || !tensor_ok(y_q, 16)) return LA_ERR_INVALID_ARG;
+    if (H_k && (!tensor_ok(k, 16) || !tensor_ok(y_k, 16))) return LA_ERR_INVALID_ARG;
+    if (!H_k) k = y_k = nullptr;
+    const bool xt = (flags & LA_ROT_X_TOKENS) != 0, yt = (flags & LA_ROT_Y_TOKENS) != 0;
+    const size_t row = (size_t)B * T * d * (dtype == LA_BF16 ? 2 : 4), qb = row * H_q, kb = row * H_k;
+    // in place (each value is read and written by one thread) where the layouts agree
+    const void *rq = (y_q == q && xt == yt) ? nullptr : q, *rk = (y_k == k && xt == yt) ? nullptr : k;
+    if (!writes_disjoint({{y_q, qb}, {y_k, kb}},
+                         {{rq, qb}, {rk, kb}, {freqs, sizeof(double) * (rotary_dim / 2)},
+                          {positions, sizeof(int) * (size_t)B * T}}))
+        return LA_ERR_INVALID_ARG;
+    RotaryArgs a;
+    a.dtype = dtype;
+    a.B = B; a.T = T; a.Hq = H_q; a.Hk = H_k; a.d = d; a.r = rotary_dim;
+    a.q = q; a.k = k; a.yq = y_q; a.yk = y_k;
+    a.freqs = freqs;
+    a.positions = positions;
+    a.start = start;
+    a.scale = scale;
+    a.interleaved = (flags & LA_ROT_INTERLEAVED) != 0;
+    a.transpose = (flags & LA_ROT_TRANSPOSE) != 0;
+    a.x_tokens = xt;
+    a.y_tokens = yt;
+    a.stream = static_cast<cudaStream_t>(stream);
+    return from_cuda(launch_rotary(a));
+}
+
+// ---------------------------------------------------------------- RMS norm
+
+namespace {
+
+constexpr int kMaxNormColumns = 16384;
+
+la_status_t norm_sizes(int dtype, int B, int H, int T, int C, float eps) {
+    if (dtype != LA_F32 && dtype != LA_BF16) return LA_ERR_INVALID_ARG;
+    if (B < 1 || H < 1 || T < 0 || C < 1 || !(eps >= 0.f)) return LA_ERR_INVALID_ARG;
+    if (C > kMaxNormColumns) return LA_ERR_UNSUPPORTED;
+    if ((long long)B * H > kMaxElems / C || (T > 0 && (long long)B * H * C > kMaxElems / T)) return LA_ERR_INVALID_ARG;
+    return LA_OK;
+}
+
+}  // namespace
+
+extern "C" la_status_t la_rms_norm(la_dtype_t dtype, int B, int H, int T, int C, const void *x,
+                                   const void *residual, const float *w, float eps, void *residual_out, void *y,
+                                   float *scales, int group, unsigned flags, void *stream) {
+    timer_reset();
+    if (flags & ~LA_NORM_FP8) return LA_ERR_INVALID_ARG;
+    const la_status_t sized = norm_sizes(dtype, B, H, T, C, eps);
+    if (sized != LA_OK) return sized;
+    const bool fp8 = (flags & LA_NORM_FP8) != 0;
+    if (group != 0 && (!fp8 || group != 128 || C % 128)) return LA_ERR_INVALID_ARG;
+    if (residual && H != 1) return LA_ERR_INVALID_ARG;
+    if (T == 0) return LA_OK;
+    if (!tensor_ok(x, 16) || !tensor_ok(w, 16) || !tensor_ok(y, 16) || (fp8 && !tensor_ok(scales, 4)))
+        return LA_ERR_INVALID_ARG;
+    if (residual && (!tensor_ok(residual, 16) || !tensor_ok(residual_out, 16))) return LA_ERR_INVALID_ARG;
+    if (!residual) residual_out = nullptr;
+    if (!fp8) scales = nullptr;
+    const size_t es = dtype == LA_BF16 ? 2 : 4, rows = (size_t)B * H * T, xb = rows * C * es;
+    // the stream may be updated in place: a thread stores what it alone has read
+    const void *rx = residual_out == x ? nullptr : x, *rr = residual_out == residual ? nullptr : residual;
+    if (!writes_disjoint({{y, rows * C * (fp8 ? 1 : es)}, {residual_out, xb},
+                          {scales, sizeof(float) * rows * (group ? C / group : 1)}},
+                         {{rx, xb}, {rr, xb}, {w, sizeof(float) * (size_t)C}}))
+        return LA_ERR_INVALID_ARG;
+    NormArgs a;
+    a.dtype = dtype;
+    a.B = B; a.H = H; a.T = T; a.C = C;
+    a.x = x; a.residual = residual; a.w = w;
+    a.h = residual_out; a.y = y; a.scales = scales;
+    a.fp8 = fp8;
+    a.group = group;
+    a.eps = eps;
+    a.stream = static_cast<cudaStream_t>(stream);
+    return from_cuda(launch_norm(a));
+}
+
+extern "C" size_t la_rms_norm_backward_workspace_size(int B, int H, int T, int C) {
+    if (norm_sizes(LA_F32, B, H, T, C, 0.f) != LA_OK || T == 0) return 0;
+    return norm_backward_partial_bytes((long long)B * H * T, C);
+}
+
+extern "C" la_status_t la_rms_norm_backward(la_dtype_t dtype, int B, int H, int T, int C, const void *h,
+                                            const float *w, float eps, const void *dy, const void *dresidual,
+                                            void *dx, float *dw, void *workspace, size_t workspace_bytes,
+                                            void *stream) {
+    timer_reset();
+    const la_status_t sized = norm_sizes(dtype, B, H, T, C, eps);
+    if (sized != LA_OK) return sized;
+    if (!tensor_ok(dw, 16)) return LA_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (T == 0) return from_cuda(cudaMemsetAsync(dw, 0, sizeof(float) * (size_t)C, st));
+    const void *need[] = {h, w, dy, dx, workspace};
+    for (const void *q : need)
+        if (!tensor_ok(q, 16)) return LA_ERR_INVALID_ARG;
+    if (dresidual && !tensor_ok(dresidual, 16)) return LA_ERR_INVALID_ARG;
+    if (workspace_bytes < la_rms_norm_backward_workspace_size(B, H, T, C)) return LA_ERR_INVALID_ARG;
+    const size_t xb = (size_t)B * H * T * C * (dtype == LA_BF16 ? 2 : 4), wb = sizeof(float) * (size_t)C;
+    if (!writes_disjoint({{dx, xb}, {dw, wb}, {workspace, workspace_bytes}},
+                         {{h, xb}, {w, wb}, {dy, xb}, {dresidual, xb}}))
+        return LA_ERR_INVALID_ARG;
+    NormBackwardArgs a;
+    a.dtype = dtype;
+    a.B = B; a.H = H; a.T = T; a.C = C;
+    a.h = h; a.dy = dy; a.dres = dresidual; a.w = w;
+    a.dx = dx; a.dw = dw;
+    a.partial = static_cast<float *>(workspace);
+    a.eps = eps;
+    a.stream = st;
+    return from_cuda(launch_norm_backward(a));
+}

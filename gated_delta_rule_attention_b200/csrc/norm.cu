@@ -24,8 +24,7 @@
 // weights stay in registers or L1.  dw: every thread keeps its columns' sums over its CTA's rows in
 // registers, each CTA writes one row of partial sums, and a second kernel adds those in a fixed
 // order.
-#include "la_internal.cuh"
-#include "vec.cuh"
+#include "layer.h"
 
 #include <atomic>
 #include <cuda_fp8.h>

@@ -20,8 +20,7 @@
 // and applies them to every HS-th head of q and of k, several heads' loads in flight; the
 // HS threads of a token that hold the same pairs, and then the pairs of a head, are
 // neighbours, so a warp reads and writes whole 256-byte head rows.
-#include "la_internal.cuh"
-#include "vec.cuh"
+#include "layer.h"
 
 #include <type_traits>
 

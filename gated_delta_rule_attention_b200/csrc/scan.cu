@@ -40,9 +40,8 @@
 // latencies (barrier, shared-memory reads, fold: 1.0 to 1.3 us a tile), so with few columns the
 // time axis goes over K CTAs and walk 1 of the next step comes before walk 2 of this one (AHEAD):
 // the runs travel meanwhile (B1 T50001 C192 fp32: 32 us, floor 18; 42 without AHEAD).
-#include "scan_util.cuh"
+#include "scan_util.h"
 #include "tmap.cuh"
-#include "vec.cuh"
 
 #include <cmath>
 #include <initializer_list>

@@ -1,8 +1,8 @@
-// scan_util.cuh -- row codes of packed batches, parameters, and the choice of a variant and a cluster
+// scan_util.h -- row codes of packed batches, parameters, and the choice of a variant and a cluster
 // width for the gated linear recurrence (scan.cu).
 #pragma once
 
-#include "la_internal.cuh"
+#include "layer.h"
 #include "ptx.cuh"
 
 #include <atomic>
