@@ -200,59 +200,58 @@ struct Shape {
 };
 constexpr uint32_t whole(uint32_t n) { return (n + 127) / 128 * 128; }
 
-// One stage of the ring: the tile's gates, x (dh), then packed batches' row codes or the
-// backward pass's checkpoint rows (one for each 32 rows).
-template <typename IO, typename SH, bool TMA>
-struct ScanStage {
-    static constexpr uint32_t kGate = SH::TT * SH::CH * sizeof(float), kX = SH::TT * SH::CH * (TMA ? sizeof(IO) : 4);
-    static constexpr uint32_t bytes(bool packed) { return whole(kGate + kX + (packed ? SH::TT * 4 : 0)); }
-};
-template <typename IO, typename SH, bool TMA>
-struct BackwardStage {
-    static constexpr uint32_t kGate = SH::TT * SH::CH * sizeof(float), kX = SH::TT * SH::CH * (TMA ? sizeof(IO) : 4);
-    static constexpr uint32_t kKept = kGate + 2 * kX;
-    static constexpr int kSpans = SH::TT / kScanCheckpoint;
-    static constexpr uint32_t bytes() { return whole(kKept + kSpans * SH::CH * sizeof(float)); }
-};
-
-// Rows that TMA cannot take (V = 1): every lane copies its own channel's values into its own
-// places of the ring, 4 bytes at a time, and reads nothing else, so it waits for its own copies
-// alone.  A bf16 value comes with the aligned word it lies in, of which the lane picks its half;
-// the first and the last word of a tensor could reach beyond it, so the tiles that hold those
-// take their values singly.
-__device__ __forceinline__ void copy_word(void *dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
-}
+// Rows that TMA cannot take: every lane copies its own channels' values into its own places of the
+// ring, and reads nothing else, so it waits for its own copies alone.  A single bf16 value (V = 1)
+// comes with the aligned 4-byte word it lies in, of which the lane picks its half; the first and
+// the last word of a tensor could reach beyond it, so the tiles that hold those take their values
+// singly.
+template <typename IO, int V>
+constexpr bool kByWord = sizeof(IO) * V < 4;
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// n rows of a lane's channel, `pitch` values apart, to places `to` a row apart.
-template <int ROW>
-__device__ __forceinline__ void copy_rows(uint32_t *to, const float *from, long long pitch, int n, bool) {
-#pragma unroll 4
-    for (int s = 0; s < n; ++s) copy_word(to + s * ROW, from + s * pitch);
+template <int BYTES>
+__device__ __forceinline__ void copy_bytes(void *dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(ptx::smem_u32(dst)), "l"(src), "n"(BYTES) : "memory");
 }
-template <int ROW>
-__device__ __forceinline__ void copy_rows(uint32_t *to, const __nv_bfloat16 *from, long long pitch, int n, bool edge) {
-    const uint16_t *at = reinterpret_cast<const uint16_t *>(from);
-    if (edge) {
-        for (int s = 0; s < n; ++s) to[s * ROW] = at[s * pitch] * 0x10001u;   // in both halves
+// n rows of a lane's V channels, `pitch` values apart, to places ROW lanes' V values apart.
+template <int V, int ROW, typename IO>
+__device__ __forceinline__ void copy_rows(unsigned char *to, const IO *from, long long pitch, int n, bool edge) {
+    if constexpr (kByWord<IO, V>) {
+        const uint16_t *at = reinterpret_cast<const uint16_t *>(from);
+        if (edge) {
+            for (int s = 0; s < n; ++s) reinterpret_cast<uint32_t *>(to)[s * ROW] = at[s * pitch] * 0x10001u;   // both halves
+        } else {
+#pragma unroll 4
+            for (int s = 0; s < n; ++s)
+                copy_bytes<4>(to + s * ROW * 4, reinterpret_cast<const void *>(reinterpret_cast<uintptr_t>(at + s * pitch) & ~(uintptr_t)3));
+        }
     } else {
 #pragma unroll 4
-        for (int s = 0; s < n; ++s)
-            copy_word(to + s * ROW, reinterpret_cast<const void *>(reinterpret_cast<uintptr_t>(at + s * pitch) & ~(uintptr_t)3));
+        for (int s = 0; s < n; ++s) copy_bytes<V * (int)sizeof(IO)>(to + s * ROW * (int)sizeof(IO), from + s * pitch);
     }
 }
-// Row s of copied values: `from` is the tensor's place of the lane's row 0.
-__device__ __forceinline__ void pick_word(Raw<float, 1> &x, uint32_t word, const float *, long long) {
-    x.v.v = __uint_as_float(word);
+// The half of a copied word that is value `off` from `from`.
+__device__ __forceinline__ uint16_t pick_half(uint32_t word, const void *from, long long off) {
+    return (uint16_t)((reinterpret_cast<uintptr_t>(from) / 2 + (uintptr_t)off) & 1 ? word >> 16 : word);
 }
-__device__ __forceinline__ void pick_word(Raw<__nv_bfloat16, 1> &x, uint32_t word, const __nv_bfloat16 *from, long long off) {
-    const bool high = (reinterpret_cast<uintptr_t>(from) / 2 + (uintptr_t)off) & 1;
-    x.v = (uint16_t)(high ? word >> 16 : word);
-}
+
+// One stage of the ring: the tile's gates, x (dh), then packed batches' row codes or the
+// backward pass's checkpoint rows (one for each 32 rows).
+template <typename IO, typename SH, bool TMA>
+struct ScanStage {
+    static constexpr uint32_t kGate = SH::TT * SH::CH * sizeof(float), kX = SH::TT * SH::CH * (!TMA && kByWord<IO, SH::V> ? 4 : sizeof(IO));
+    static constexpr uint32_t bytes(bool packed) { return whole(kGate + kX + (packed ? SH::TT * 4 : 0)); }
+};
+template <typename IO, typename SH, bool TMA>
+struct BackwardStage {
+    static constexpr uint32_t kGate = SH::TT * SH::CH * sizeof(float), kX = SH::TT * SH::CH * (!TMA && kByWord<IO, SH::V> ? 4 : sizeof(IO));
+    static constexpr uint32_t kKept = kGate + 2 * kX;
+    static constexpr int kSpans = SH::TT / kScanCheckpoint;
+    static constexpr uint32_t bytes() { return whole(kKept + kSpans * SH::CH * sizeof(float)); }
+};
 
 // Shared memory: the ring of stages, then this, then (on 16 bytes) Run slot[kSlots][K][32].
 template <int V, int STAGES>
@@ -342,7 +341,7 @@ struct Rows {
 
 template <typename IO, typename SH, int STAGES, bool BLEND, bool PACKED, bool AHEAD, bool TMA>
 __global__ void __launch_bounds__(kThreads, AHEAD ? 1 : 2) scan_kernel(const __grid_constant__ KernelParams q) {
-    static_assert(TMA || SH::V == 1, "copied rows have one channel a lane");
+    constexpr bool kWords = !TMA && kByWord<IO, SH::V>;
     constexpr int V = SH::V, S = SH::S, CH = SH::CH, TT = SH::TT;
     using L = Lane<V>;
     using St = ScanStage<IO, SH, TMA>;
@@ -374,11 +373,12 @@ __global__ void __launch_bounds__(kThreads, AHEAD ? 1 : 2) scan_kernel(const __g
                 unsigned char *at = ring + (size_t)(step % STAGES) * kStage;
                 if (act) {
                     const bool edge = (b == 0 && w0 == 0) || (b == p.B - 1 && w0 + S >= T);
-                    copy_rows<CH>(reinterpret_cast<uint32_t *>(at) + warp * S * CH + lane, p.gate + (b * T + w0) * C + c0, C, n, false);
-                    copy_rows<CH>(reinterpret_cast<uint32_t *>(at + St::kGate) + warp * S * CH + lane, xc + w0 * C, C, n, edge);
+                    const int o = warp * S * CH + lane * V;
+                    copy_rows<V, CH>(at + o * 4, p.gate + (b * T + w0) * C + c0, C, n, false);
+                    copy_rows<V, CH>(at + St::kGate + o * (kWords ? 4 : sizeof(IO)), xc + w0 * C, C, n, edge);
                 }
                 // codes exist in whole tiles, zeros behind the last row
-                if (PACKED && lane < S) copy_word(at + St::kGate + St::kX + (warp * S + lane) * 4, p.codes + w0 + lane);
+                if (PACKED && lane < S) copy_bytes<4>(at + St::kGate + St::kX + (warp * S + lane) * 4, p.codes + w0 + lane);
             }
             copy_commit();
             return;
@@ -422,12 +422,12 @@ __global__ void __launch_bounds__(kThreads, AHEAD ? 1 : 2) scan_kernel(const __g
             IO *sx = reinterpret_cast<IO *>(at + St::kGate) + warp * S * CH + lane * V;
             uint32_t *sw = reinterpret_cast<uint32_t *>(at + St::kGate) + warp * S * CH + lane;   // copied words
             auto take = [&](Raw<IO, V> &x, int s) {
-                if constexpr (TMA) x.load(sx + s * CH);
-                else pick_word(x, sw[s * CH], xc, (t0 + s) * C);
+                if constexpr (kWords) x.v = pick_half(sw[s * CH], xc, (t0 + s) * C);
+                else x.load(sx + s * CH);
             };
             auto clear = [&](int s) {
-                if constexpr (TMA) L::all(0.f).store(sx + s * CH);
-                else sw[s * CH] = 0;
+                if constexpr (kWords) sw[s * CH] = 0;
+                else L::all(0.f).store(sx + s * CH);
             };
             if constexpr (PACKED) {
                 // Rows of no sequence get a = 1, x = 0, which leaves the state.  A sequence's first
@@ -583,7 +583,7 @@ struct BackwardRows {
 template <typename IO, typename SH, int STAGES, bool BLEND, bool AHEAD, bool TMA>
 __global__ void __launch_bounds__(kThreads, AHEAD ? 1 : 2)
 scan_backward_kernel(const __grid_constant__ BackwardKernelParams q) {
-    static_assert(TMA || SH::V == 1, "copied rows have one channel a lane");
+    constexpr bool kWords = !TMA && kByWord<IO, SH::V>;
     constexpr int V = SH::V, S = SH::S, CH = SH::CH, TT = SH::TT;
     constexpr int kGroups = kScanCheckpoint / S;   // warps between two checkpoints
     static_assert(kScanCheckpoint % S == 0 && TT % kScanCheckpoint == 0, "tiles hold whole checkpoint spans");
@@ -618,13 +618,13 @@ scan_backward_kernel(const __grid_constant__ BackwardKernelParams q) {
             if (step < p.steps && w0 >= 0 && w0 < T && act) {
                 const int n = T - w0 < S ? (int)(T - w0) : S;
                 unsigned char *at = ring + (size_t)(step % STAGES) * kStage;
-                const int o = warp * S * CH + lane;
+                const int o = warp * S * CH + lane * V, ox = o * (kWords ? 4 : (int)sizeof(IO));
                 const bool edge = (b == 0 && w0 == 0) || (b == p.B - 1 && w0 + S >= T);
-                copy_rows<CH>(reinterpret_cast<uint32_t *>(at) + o, p.gate + (b * T + w0) * C + c0, C, n, false);
-                copy_rows<CH>(reinterpret_cast<uint32_t *>(at + St::kGate) + o, xc + w0 * C, C, n, edge);
-                copy_rows<CH>(reinterpret_cast<uint32_t *>(at + St::kGate + St::kX) + o, dc + w0 * C, C, n, edge);
+                copy_rows<V, CH>(at + o * 4, p.gate + (b * T + w0) * C + c0, C, n, false);
+                copy_rows<V, CH>(at + St::kGate + ox, xc + w0 * C, C, n, edge);
+                copy_rows<V, CH>(at + St::kGate + St::kX + ox, dc + w0 * C, C, n, edge);
                 if (kept)
-                    copy_word(at + St::kKept + (warp / kGroups * CH + lane) * 4, p.ckpt + (b * rows + w0 / kScanCheckpoint) * C + c0);
+                    copy_bytes<4 * V>(at + St::kKept + (warp / kGroups * CH + lane * V) * 4, p.ckpt + (b * rows + w0 / kScanCheckpoint) * C + c0);
             }
             copy_commit();
             return;
@@ -665,12 +665,12 @@ scan_backward_kernel(const __grid_constant__ BackwardKernelParams q) {
 #pragma unroll
             for (int s = 0; s < S; ++s) {
                 w.a[s] = L::load(reinterpret_cast<const float *>(at) + o + s * CH);
-                if constexpr (TMA) {
+                if constexpr (kWords) {
+                    w.x[s].v = pick_half(reinterpret_cast<const uint32_t *>(at + St::kGate)[o + s * CH], xc, (t0 + s) * C);
+                    w.d[s].v = pick_half(reinterpret_cast<const uint32_t *>(at + St::kGate + St::kX)[o + s * CH], dc, (t0 + s) * C);
+                } else {
                     w.x[s].load(reinterpret_cast<const IO *>(at + St::kGate) + o + s * CH);
                     w.d[s].load(reinterpret_cast<const IO *>(at + St::kGate + St::kX) + o + s * CH);
-                } else {
-                    pick_word(w.x[s], reinterpret_cast<const uint32_t *>(at + St::kGate)[o + s * CH], xc, (t0 + s) * C);
-                    pick_word(w.d[s], reinterpret_cast<const uint32_t *>(at + St::kGate + St::kX)[o + s * CH], dc, (t0 + s) * C);
                 }
             }
             if (kept && act && t0 < T)
@@ -933,10 +933,14 @@ bool rows_by_tma(const ScanBackwardArgs &a) {
 //   one CTA an SM, AHEAD, K = 1 .. 16: few columns, and with a ring of 144 KB and more also the
 //   fastest where 32-channel columns fill the SMs once (B2 T32768 C2048 bf16: 167 us against 172).
 // V = 2 has half the columns and 256-byte gate rows, V = 1 twice the CTAs.
-// Rows that TMA cannot take are bound by their lanes' copies (two a value, 4 bytes each): B2
-// T5000 C1001 bf16 38 us, floor 12.
+// Rows that TMA cannot take are bound by their lanes' copies, two channels at a time where C and
+// the starts are even (B2 T5000 C1002 bf16 28 us, floor 12), else one (C1001 40 us).
 template <typename IO, bool BLEND, bool PACKED>
 cudaError_t forward(const ScanArgs &a) {
+    if (!rows_by_tma(a) && vector_width<IO>(a.C, {a.x, a.h}, {a.gate, a.ckpt, a.state_in, a.state_out}) > 1)
+        return launch_best<Forward<IO, Shape<2, 16>, 3, BLEND, PACKED, false, 4, 1500, 150, 4000, false>,
+                           Forward<IO, Shape<2, 32>, 3, BLEND, PACKED, true, 16, 2000, 150, 4000, false>,
+                           Forward<IO, Shape<1, 32>, 3, BLEND, PACKED, true, 16, 2350, 150, 2600, false>>(a);
     if (!rows_by_tma(a))
         return launch_best<Forward<IO, Shape<1, 16>, 3, BLEND, PACKED, false, 4, 1500, 150, 3200, false>,
                            Forward<IO, Shape<1, 32>, 3, BLEND, PACKED, true, 16, 2350, 150, 2600, false>>(a);
@@ -962,6 +966,9 @@ cudaError_t forward_io(const ScanArgs &a) {
 // of its CTAs is faster alone), and has few columns go AHEAD.
 template <typename IO, bool BLEND>
 cudaError_t backward(const ScanBackwardArgs &a) {
+    if (!rows_by_tma(a) && vector_width<IO>(a.C, {a.x, a.dh, a.dx}, {a.gate, a.ckpt, a.dgate, a.dstate, a.dstate0}) > 1)
+        return launch_best<Backward<IO, Shape<2, 16>, 2, BLEND, false, 8, 1550, 150, 4000, false>,
+                           Backward<IO, Shape<1, 16>, 4, BLEND, true, 16, 2600, 130, 2100, false>>(a);
     if (!rows_by_tma(a))
         return launch_best<Backward<IO, Shape<1, 8>, 3, BLEND, false, 4, 1650, 150, 3000, false>,
                            Backward<IO, Shape<1, 16>, 4, BLEND, true, 16, 2600, 130, 2100, false>>(a);
