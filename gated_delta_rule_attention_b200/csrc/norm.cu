@@ -96,9 +96,32 @@ __device__ __forceinline__ void row_sums(float2 (&v)[ROWS], float2 (*box)[NT > 3
 }
 
 // Scale of a group whose largest |y| is `top`: 1 for zeros, and never so small that its
-// reciprocal overflows.
+// reciprocal overflows.  The products with reciprocals instead of quotients leave scale and q
+// within two half steps of fp32, far below a step of e4m3.
 __device__ __forceinline__ float fp8_scale(float top) {
-    return top > 0.f ? fmaxf(top / kFp8Max, 1.17549435e-38f) : 1.f;
+    return top > 0.f ? fmaxf(top * (1.f / kFp8Max), 1.17549435e-38f) : 1.f;
+}
+
+// x + r rounded to the stream's type.  The packed bf16 sum rounds once, and so does the fp32 sum
+// rounded to bf16: where it is inexact in fp32, the smaller value is below 2^-16 of the larger,
+// too small to move its rounding.
+template <int V>
+__device__ __forceinline__ void add_residual(Pack<float, V> &x, const Pack<float, V> &r) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) x.v[j] += r.v[j];
+}
+template <int V>
+__device__ __forceinline__ void add_residual(Pack<__nv_bfloat16, V> &x, const Pack<__nv_bfloat16, V> &r) {
+    if constexpr (V == 1) {
+        x.v[0] = __hadd(x.v[0], r.v[0]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; j += 2) {
+            const __nv_bfloat162 s = __hadd2(__nv_bfloat162(x.v[j], x.v[j + 1]), __nv_bfloat162(r.v[j], r.v[j + 1]));
+            x.v[j] = s.x;
+            x.v[j + 1] = s.y;
+        }
+    }
 }
 
 template <int V>
@@ -183,8 +206,7 @@ __global__ void __launch_bounds__(NT <= 32 ? 256 : NT, (RES && ROWS * K * V >= 3
             for (int q = 0; q < ROWS; ++q) {
                 const long long i = i0 + q * kRowsBlock;
                 if constexpr (RES) {
-#pragma unroll
-                    for (int j = 0; j < V; ++j) x[q][k].v[j] = from_f32<IO>(to_f32(x[q][k].v[j]) + to_f32(r[q][k].v[j]));
+                    add_residual<V>(x[q][k], r[q][k]);
                     if (i < p.rows && c < C) store_pack<IO, V>(static_cast<IO *>(p.h) + i * C + c, x[q][k]);
                 }
 #pragma unroll
@@ -207,7 +229,7 @@ __global__ void __launch_bounds__(NT <= 32 ? 256 : NT, (RES && ROWS * K * V >= 3
             o[q] = row * C;
             if (FP8 == 1) {
                 const float scale = fp8_scale(sum[q].y * rstd[q]);
-                inv[q] = 1.f / scale;
+                inv[q] = __fdividef(1.f, scale);
                 if (i < p.rows && t == 0) p.scales[row] = scale;
             }
         }
@@ -230,7 +252,7 @@ __global__ void __launch_bounds__(NT <= 32 ? 256 : NT, (RES && ROWS * K * V >= 3
 #pragma unroll
                     for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, off));
                     const float scale = fp8_scale(top);
-                    inv[q] = 1.f / scale;
+                    inv[q] = __fdividef(1.f, scale);
                     if (ok && (threadIdx.x & 15) == 0) p.scales[(o[q] + c) / 128] = scale;
                 }
                 if constexpr (FP8) {
