@@ -28,7 +28,6 @@ namespace la {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int MINB = 3;
 
 struct RotaryParams {
     const void *x[2];      // q, k
@@ -62,15 +61,15 @@ __device__ __forceinline__ long long row_of(bool token_major, long long b, long 
 
 // PAIRS pairs a thread: 8 (rows in 16-byte vectors; r a multiple of 16, d of 8), or 1.
 // Units behind the rotated ones copy 2 * PAIRS values (none when in place).
-// SHARE: the HS = SHARE threads that hold the same pairs of one token are lanes of one warp,
-// units apart: each forms PAIRS / SHARE of the angles and the others get them by shuffles.
+// SHARE: a warp is one token, and the HS = SHARE threads that hold the same pairs are units apart
+// in it: each forms PAIRS / SHARE of the angles and the others get them by shuffles.
 template <typename IO, int PAIRS, bool INTERLEAVED, int SHARE>
-__global__ void __launch_bounds__(kThreads, PAIRS == 1 ? 4 : MINB) rotary_kernel(const RotaryParams p) {
+__global__ void __launch_bounds__(kThreads, PAIRS == 1 ? 4 : 3) rotary_kernel(const RotaryParams p) {
     using X = Pack<IO, PAIRS>;
     const long long idx = (long long)blockIdx.x * kThreads + threadIdx.x;
     long long token;
     int u, hs;
-    if (p.tokens * p.units * p.HS <= UINT32_MAX) {
+    if (p.tokens * p.units * p.HS <= UINT32_MAX - kThreads) {   // the last block's indexes too
         const unsigned i = (unsigned)idx;
         u = i % (unsigned)p.units;
         hs = i / (unsigned)p.units % (unsigned)p.HS;
@@ -80,7 +79,7 @@ __global__ void __launch_bounds__(kThreads, PAIRS == 1 ? 4 : MINB) rotary_kernel
         hs = (int)(idx / p.units % p.HS);
         token = idx / p.units / p.HS;
     }
-    if (token >= p.tokens) return;   // with SHARE: a token's threads go or stay together
+    if (token >= p.tokens) return;   // with SHARE: whole warps
     const long long b = token / p.T, t = token - b * p.T;
     const int turned = p.r / (2 * PAIRS);
     const bool turn = u < turned;
@@ -102,12 +101,11 @@ __global__ void __launch_bounds__(kThreads, PAIRS == 1 ? 4 : MINB) rotary_kernel
 #pragma unroll
         for (int j = 0; j < kOwn; ++j)
             if (turn) angle(pos, p.freqs[u * PAIRS + hs * kOwn + j], s[j], c[j]);
-        const unsigned here = __activemask();
         const int lane = threadIdx.x & 31, first = lane - hs * p.units;   // the lane of hs = 0
 #pragma unroll
         for (int j = 0; j < PAIRS; ++j) {
-            cs[j] = __shfl_sync(here, c[j % kOwn], first + j / kOwn * p.units);
-            sn[j] = __shfl_sync(here, s[j % kOwn], first + j / kOwn * p.units);
+            cs[j] = __shfl_sync(~0u, c[j % kOwn], first + j / kOwn * p.units);
+            sn[j] = __shfl_sync(~0u, s[j % kOwn], first + j / kOwn * p.units);
         }
     } else if (turn) {
 #pragma unroll

@@ -726,31 +726,41 @@ scan_backward_kernel(const __grid_constant__ BackwardKernelParams q) {
         else run = fma(w.tile.P, run, w.tile.H);
         const long long t0 = tile_row(step) + warp * S;
         if (!act || t0 < 0 || t0 >= T) return;
-        L before[S], h = w.front, m = fma(w.behind.P, in, w.behind.H);
+        L before[S], h = w.front;
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             before[s] = h;
             h = fma(w.a[s], h, BLEND ? blended(w.a[s], w.x[s].wide()) : w.x[s].wide());
         }
-        auto row = [&](int s, IO *to, float *tg) {
-            const L l = add(w.d[s].wide(), m);
-            m = mul(w.a[s], l);
-            (BLEND ? blended(w.a[s], l) : l).store(to);
-            if (tg) mul(l, BLEND ? sub(before[s], w.x[s].wide()) : before[s]).store(tg);
+        // l_t = dh_t + a_{t+1} l_{t+1}; rows behind the end have a = 1 and dh = 0
+        L l = add(w.d[S - 1].wide(), fma(w.behind.P, in, w.behind.H));
+        auto back = [&](int s) {
+            if (s < S - 1) l = fma(w.a[s + 1 < S ? s + 1 : s], l, w.d[s].wide());
         };
-        IO *to = ob + (t0 + S - 1) * C;
+        auto put = [&](int s, IO *to) { (BLEND ? blended(w.a[s], l) : l).store(to); };
+        auto put_gate = [&](int s, float *to) {
+            mul(l, BLEND ? sub(before[s], w.x[s].wide()) : before[s]).store(to);
+        };
         if (t0 + S <= T && gb) {
+            IO *to = ob + (t0 + S - 1) * C;
             float *tg = gb + (t0 + S - 1) * C;
 #pragma unroll
             for (int s = S - 1; s >= 0; --s) {
-                row(s, to, tg);
+                back(s);
+                put(s, to);
+                put_gate(s, tg);
                 to -= C;
                 tg -= C;
             }
         } else {
 #pragma unroll
-            for (int s = S - 1; s >= 0; --s)
-                if (t0 + s < T) row(s, ob + (t0 + s) * C, gb ? gb + (t0 + s) * C : nullptr);
+            for (int s = S - 1; s >= 0; --s) {
+                back(s);
+                if (t0 + s < T) {
+                    put(s, ob + (t0 + s) * C);
+                    if (gb) put_gate(s, gb + (t0 + s) * C);
+                }
+            }
         }
     };
     R w;

@@ -190,3 +190,39 @@ def test_launches_are_counted_and_timed(la):
     finally:
         la.launch_timing(False)
     assert len(times) == 2 and all(t > 0 for t in times)
+
+
+FIRST = """
+import torch
+import gated_delta_rule_attention_b200 as la
+x = torch.randn(2, 100, 256, device="cuda").to(torch.bfloat16)
+gate = torch.rand(2, 100, 256, device="cuda")
+w, wh = torch.ones(256, device="cuda"), torch.ones(64, device="cuda")
+cu = torch.tensor([0, 50, 200], dtype=torch.int32, device="cuda")
+freqs, _ = la.rotary_frequencies(64)
+def run():
+    h, s, kept = la.linear_scan(x, gate, checkpoints=True)
+    out = [h, s, *la.linear_scan_backward(x, gate, x, checkpoints=kept, need_dstate0=True)]
+    out += la.linear_scan_varlen(x.view(-1, 256), gate.view(-1, 256), cu)
+    q = la.rotary(x, freqs=freqs, d=64)
+    out += [q, la.rms_norm_heads(q, wh), *la.rms_norm_backward(x, w, x)]
+    return out
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):   # the library's first calls in this process
+    got = run()
+g.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, run()))
+la.check_status()
+print("same")
+"""
+
+
+def test_first_calls_may_be_captured(tmp_path):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]

@@ -187,3 +187,24 @@ def test_norm_gradient_against_differences(la):
         num = float(((f(t + e * d).double() - f(t - e * d).double()) * dy).sum()) / (2 * e)
         want = float((grad.double() * d).sum())
         assert num == pytest.approx(want, rel=2e-3, abs=2e-3 * float((grad.double() * d).norm()))
+
+
+def test_norm_offsets_beyond_32_bits(la):
+    R, C = 2 ** 31 // 1024 + 9, 1024
+    x = torch.empty(R, C, dtype=torch.bfloat16, device="cuda").uniform_(-1, 1)
+    w = 1 + 0.3 * rand(torch.float32, C, seed=2)
+    y, h = la.rms_norm(x, w, residual=x)
+    tail = la.rms_norm(x[-20:], w, residual=x[-20:])
+    assert torch.equal(y[-20:], tail[0]) and torch.equal(h[-20:], tail[1])
+    q, s = la.rms_norm(x, w, fp8=True, group=128)
+    qt, st = la.rms_norm(x[-20:], w, fp8=True, group=128)
+    assert torch.equal(q[-20:].view(torch.uint8), qt.view(torch.uint8)) and torch.equal(s[-20:], st)
+    dx, _ = la.rms_norm_backward(x, w, h)
+    assert torch.equal(dx[-20:], la.rms_norm_backward(x[-20:], w, h[-20:])[0])
+    T = 2 ** 31 // 256 + 5   # two heads of 128
+    o = x.view(-1)[:2 * T * 128].view(1, 2, T, 128)
+    yh = la.rms_norm_heads(o, w[:128].contiguous())
+    for head in (0, 1):
+        want = la.rms_norm(o[0, head, -9:], w[:128].contiguous())
+        assert torch.equal(yh[0, -9:, head * 128:(head + 1) * 128], want)
+    la.check_status()

@@ -141,3 +141,15 @@ def test_rotary_empty_and_refusals(la):
     with pytest.raises(la.LaError, match="UNSUPPORTED"):
         la.rotary(torch.zeros(1, 1, 1024, device="cuda"), freqs=freqs, d=1024)
     la.check_status()
+
+
+def test_rotary_offsets_beyond_32_bits(la):
+    T, H, d = 2 ** 31 // 512 + 33, 4, 128
+    q = torch.empty(1, T, H * d, dtype=torch.bfloat16, device="cuda").uniform_(-1, 1)
+    freqs, _ = la.rotary_frequencies(d)
+    y = la.rotary(q, freqs=freqs, d=d)
+    tail = la.rotary(q[:, -40:].contiguous(), freqs=freqs, d=d, start=T - 40)
+    la.check_status()
+    assert torch.equal(y[:, :, -40:], tail)
+    back = la.rotary_backward(y, freqs=freqs, token_major=True)
+    assert torch.equal(back[:, -40:], la.rotary_backward(tail, freqs=freqs, start=T - 40, token_major=True))

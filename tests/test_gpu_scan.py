@@ -329,3 +329,38 @@ def test_scan_gradient_against_differences(la):
         args[0][i], args[1][i] = t + e * d, t - e * d
         num = (loss(*args[0]) - loss(*args[1])) / (2 * e)
         assert num == pytest.approx(float((grad.double() * d).sum()), rel=tol, abs=tol * float((grad.double() * d).norm()))
+
+
+@pytest.mark.parametrize("C", [64, 34, 7])
+@pytest.mark.parametrize("blend", [False, True])
+def test_scan_backward_without_the_gates(la, C, blend):
+    x, gate, h0 = inputs(torch.bfloat16, 2, 150, C, seed=C)
+    want = la.linear_scan_backward(x, gate, x, state0=h0, blend=blend)
+    got = la.linear_scan_backward(x, gate, x, state0=h0, blend=blend, need_dgate=False, need_dstate0=False)
+    la.check_status()
+    assert got[1] is None and got[2] is None and torch.equal(got[0], want[0])
+
+
+@pytest.mark.parametrize("C", [4096, 4094, 4095])
+def test_scan_offsets_beyond_32_bits(la, C):
+    """More than 2^31 elements: closed gates 500 rows before the end make the last rows those of a
+    short call on them."""
+    T = 2 ** 31 // C + 700
+    x = torch.empty(1, T, C, dtype=torch.bfloat16, device="cuda").uniform_(-1, 1)
+    gate = torch.empty(1, T, C, device="cuda").uniform_(0.5, 1)
+    gate[:, T - 500] = 0
+    h, state, kept = la.linear_scan(x, gate, checkpoints=True)
+    dx, dgate, _ = la.linear_scan_backward(x, gate, x, checkpoints=kept)
+    tx, tg = x[:, T - 500:].contiguous(), gate[:, T - 500:].contiguous()
+    rh, rs, b = L.linear_scan(f64(tx), f64(tg))
+    refs, bounds = L.linear_scan_backward(f64(tx), f64(tg), f64(tx))
+    la.check_status()
+    close(h[:, T - 500:], rh, b)
+    close(state, rs, b[:, -1])
+    close(dx[:, T - 500:], refs[0], bounds[0])
+    close(dgate[:, T - 499:], refs[1][:, 1:], bounds[1][:, 1:])
+    # and the first rows, whose gradients end the reverse walk
+    gate[:, 500] = 0
+    dx, _, _ = la.linear_scan_backward(x, gate, x, need_dgate=False)
+    refs, bounds = L.linear_scan_backward(f64(x[:, :501]), f64(gate[:, :501]), f64(x[:, :501]))
+    close(dx[:, :500], refs[0][:, :500], bounds[0][:, :500])
