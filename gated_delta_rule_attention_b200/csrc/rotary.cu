@@ -16,10 +16,14 @@
 // turns are dropped, and the rest of a turn, at most 1/2, goes to sincospif.
 //
 // Bound by HBM: every value is read once and written once, two products a value.  A thread
-// owns eight pairs (two 16-byte vectors of bf16) of one token, forms their eight angles once
-// and applies them to every HS-th head of q and of k, several heads' loads in flight; the
+// owns two 16-byte vectors (eight pairs of bf16, four of fp32) of one token, forms their angles
+// once and applies them to every HS-th head of q and of k, two heads' loads in flight; the
 // HS threads of a token that hold the same pairs, and then the pairs of a head, are
-// neighbours, so a warp reads and writes whole 256-byte head rows.
+// neighbours, so a warp reads and writes whole 256-byte pieces of head rows.
+// B8 T8192 H16 d128 bf16, q and k: 173 us (95 % of the copy rate; 271 when each thread formed all
+// its angles and took a head at a time).  B1 T9001 H32 + 8 d128 fp32, 32 turned, interleaved: 64 us
+// (floor 56; 76 with a thread's two vectors next to each other, which leaves half a line to each
+// access).
 #include "layer.h"
 
 #include <type_traits>
@@ -59,7 +63,9 @@ __device__ __forceinline__ long long row_of(bool token_major, long long b, long 
     return token_major ? (b * T + t) * (long long)H * d : (b * H * T + t) * d;
 }
 
-// PAIRS pairs a thread: 8 (rows in 16-byte vectors; r a multiple of 16, d of 8), or 1.
+// PAIRS pairs a thread, in two vectors of PAIRS values: 16-byte ones (r a multiple of two, d of
+// one), or single values.  The two are half of the turned part, or of the copied one, apart, so that
+// neighbouring threads have neighbouring vectors; only a single interleaved pair lies together.
 // Units behind the rotated ones copy 2 * PAIRS values (none when in place).
 // SHARE: a warp is one token, and the HS = SHARE threads that hold the same pairs are units apart
 // in it: each forms PAIRS / SHARE of the angles and the others get them by shuffles.
@@ -84,14 +90,19 @@ __global__ void __launch_bounds__(kThreads, PAIRS == 1 ? 4 : 3) rotary_kernel(co
     const int turned = p.r / (2 * PAIRS);
     const bool turn = u < turned;
     // the two vectors of the thread in a head row
+    constexpr bool kSingle = INTERLEAVED && PAIRS == 1;
     int e0, e1;
     if (turn) {
-        e0 = INTERLEAVED ? u * 2 * PAIRS : u * PAIRS;
-        e1 = INTERLEAVED ? e0 + PAIRS : e0 + p.r / 2;
+        e0 = kSingle ? 2 * u : u * PAIRS;
+        e1 = kSingle ? e0 + 1 : e0 + p.r / 2;
     } else {
-        e0 = p.r + (u - turned) * 2 * PAIRS;
-        e1 = e0 + PAIRS;
+        e0 = p.r + (u - turned) * PAIRS;
+        e1 = e0 + (p.units - turned) * PAIRS;
     }
+    auto freq = [&](int j) {   // of the thread's pair j
+        if (!INTERLEAVED || PAIRS == 1) return p.freqs[u * PAIRS + j];
+        return p.freqs[j < PAIRS / 2 ? u * (PAIRS / 2) + j : u * (PAIRS / 2) + p.r / 4 + j - PAIRS / 2];
+    };
     const bool second = e1 < p.d;   // false: the last copied vector of a row stands alone
     float cs[PAIRS], sn[PAIRS];
     const double pos = (double)(p.positions ? (long long)p.positions[token] : p.start + t);
@@ -100,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, PAIRS == 1 ? 4 : 3) rotary_kernel(co
         float c[kOwn], s[kOwn];
 #pragma unroll
         for (int j = 0; j < kOwn; ++j)
-            if (turn) angle(pos, p.freqs[u * PAIRS + hs * kOwn + j], s[j], c[j]);
+            if (turn) angle(pos, freq(hs * kOwn + j), s[j], c[j]);
         const int lane = threadIdx.x & 31, first = lane - hs * p.units;   // the lane of hs = 0
 #pragma unroll
         for (int j = 0; j < PAIRS; ++j) {
@@ -109,7 +120,7 @@ __global__ void __launch_bounds__(kThreads, PAIRS == 1 ? 4 : 3) rotary_kernel(co
         }
     } else if (turn) {
 #pragma unroll
-        for (int j = 0; j < PAIRS; ++j) angle(pos, p.freqs[u * PAIRS + j], sn[j], cs[j]);
+        for (int j = 0; j < PAIRS; ++j) angle(pos, freq(j), sn[j], cs[j]);
     }
 #pragma unroll
     for (int j = 0; j < PAIRS; ++j) {
@@ -184,14 +195,14 @@ cudaError_t launch_pairs(const RotaryArgs &a) {
     p.y_tokens = a.y_tokens;
     const bool in_place = a.yq == a.q && (a.Hk == 0 || a.yk == a.k);
     p.units = a.r / (2 * PAIRS) + (in_place ? 0 : (a.d - a.r + 2 * PAIRS - 1) / (2 * PAIRS));
-    // Four threads a token share its heads (eight where the units of a row are four, so that they
-    // fill a warp); more of them where the tokens alone would leave the SMs with less than a few
-    // warps each (decoding).
+    // Four threads a token share its heads (eight where the units of a row are four, two where they
+    // are 16, so that they fill a warp); more of them where the tokens alone would leave the SMs
+    // with less than a few warps each (decoding).
     const int heads = a.Hq + a.Hk;
-    const int usual = p.units == 4 ? 8 : 4;
+    const int usual = p.units == 4 ? 8 : p.units == 16 ? 2 : 4;
     p.HS = heads < usual ? heads : usual;
     while (p.HS < heads && p.tokens * p.units * p.HS < 148ll * 512) p.HS = 2 * p.HS < heads ? 2 * p.HS : heads;
-    const bool share = PAIRS == 8 && p.units * p.HS == 32 && (p.HS == 4 || p.HS == 8);
+    const bool share = PAIRS > 1 && p.units * p.HS == 32;
     const long long blocks = (p.tokens * p.units * p.HS + kThreads - 1) / kThreads;
     if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
     timer_begin(a.stream);
@@ -200,10 +211,12 @@ cudaError_t launch_pairs(const RotaryArgs &a) {
             <<<(unsigned)blocks, kThreads, 0, a.stream>>>(p);
     };
     auto pick = [&](auto turn_next) {
-        if constexpr (PAIRS == 8) {
+        if constexpr (PAIRS > 1) {
+            if (share && p.HS == 2) return go(turn_next, std::integral_constant<int, 2>{});
             if (share && p.HS == 4) return go(turn_next, std::integral_constant<int, 4>{});
-            if (share) return go(turn_next, std::integral_constant<int, 8>{});
         }
+        if constexpr (PAIRS > 4)
+            if (share && p.HS == 8) return go(turn_next, std::integral_constant<int, 8>{});
         go(turn_next, std::integral_constant<int, 1>{});
     };
     if (a.interleaved) pick(std::true_type{});
@@ -215,7 +228,8 @@ cudaError_t launch_pairs(const RotaryArgs &a) {
 
 template <typename IO>
 cudaError_t launch_io(const RotaryArgs &a) {
-    return a.r % 16 == 0 && a.d % 8 == 0 ? launch_pairs<IO, 8>(a) : launch_pairs<IO, 1>(a);
+    constexpr int kVector = 16 / sizeof(IO);
+    return a.r % (2 * kVector) == 0 && a.d % kVector == 0 ? launch_pairs<IO, kVector>(a) : launch_pairs<IO, 1>(a);
 }
 
 }  // namespace

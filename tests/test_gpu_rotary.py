@@ -39,10 +39,12 @@ def rand(dtype, *shape, seed=0):
 
 
 # (B, T, H, Hk, d, r): vectors and scalars (r not a multiple of 16, d not of 8), one head, shared
-# key heads, more key than query heads, parts of a head, a lone last vector (d - r = 8)
+# key heads, more key than query heads, parts of a head, a lone last vector (d - r = 8, 12), tokens
+# enough that a warp is one token whose threads share the angles
 CASES = [(1, 1, 1, 1, 64, 64), (2, 5, 3, 1, 64, 32), (1, 37, 16, 4, 128, 128), (3, 9, 5, 5, 128, 64),
          (1, 20, 1, 7, 64, 16), (2, 7, 2, 2, 24, 16), (1, 6, 4, 2, 64, 24), (1, 11, 3, 2, 10, 6),
-         (2, 3, 2, 1, 7, 2), (1, 4, 9, 0, 256, 64), (1, 3, 33, 8, 80, 80), (1, 2, 2, 1, 512, 512)]
+         (2, 3, 2, 1, 7, 2), (1, 4, 9, 0, 256, 64), (1, 3, 33, 8, 80, 80), (1, 2, 2, 1, 512, 512),
+         (2, 9, 3, 2, 36, 24), (2, 1300, 6, 2, 128, 64), (1, 2500, 5, 3, 64, 32), (1, 2400, 1, 1, 128, 128)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
