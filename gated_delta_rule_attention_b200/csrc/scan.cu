@@ -282,6 +282,10 @@ __device__ __forceinline__ void start_exchange(Exchange<V, STAGES> *ex, int K, i
         __syncthreads();
     }
 }
+// Programmatic dependent launch: what follows grid_wait sees all that the kernel in front wrote;
+// after grid_release the next kernel in the stream may start.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 // The end of the whole CTA.  After a wait that ran out, the copies still in flight get 10 ms to
 // land before the block's shared memory goes; and no CTA may leave while another one's store to
 // it is in flight.
@@ -392,10 +396,20 @@ __global__ void __launch_bounds__(kThreads, AHEAD ? 1 : 2) scan_kernel(const __g
         } else {
             ptx::mbar_arrive_expect_tx(bar, St::kX + (PACKED ? TT * 4 : 0));
             ptx::tma_load_3d(to + St::kGate, &q.x, cb, (int)t0, b, bar);
-            if (PACKED) ptx::bulk_load(to + St::kGate + St::kX, p.codes + t0, TT * 4, bar);
+            if (PACKED && step >= STAGES) ptx::bulk_load(to + St::kGate + St::kX, p.codes + t0, TT * 4, bar);
         }
     };
+    // A packed call's kernel starts while scan_rows_kernel still runs (which itself waits for all
+    // that is in front of it in the stream), asks for the first rows, and waits for the codes:
+    // 61 sequences, T20011 C1024 bf16, 51 us instead of 54.
+    if (PACKED && !TMA) grid_wait();
     for (int i = 0; i < STAGES; ++i) fetch(i);
+    if (PACKED && TMA && asks == 1) {
+        grid_wait();
+        for (int i = 0; i < STAGES && i < p.steps && tile_row(i) < T; ++i)
+            ptx::bulk_load(ptx::smem_u32(ring + (size_t)i * kStage) + St::kGate + St::kX, p.codes + tile_row(i), TT * 4,
+                           &ex->full[i]);
+    }
 
     constexpr uint32_t kAllRows = S == 32 ? ~0u : (1u << S) - 1;
     int stage = 0;
@@ -565,9 +579,9 @@ __global__ void __launch_bounds__(kThreads, AHEAD ? 1 : 2) scan_kernel(const __g
             walk2(step, w);
         }
     }
-    if (!PACKED && rank == 0 && warp == 0 && act && p.state_out) run.store(p.state_out + b * C + c0);
     if constexpr (!TMA) copy_wait<0>();
-    end_exchange(ex, K);
+    end_exchange(ex, K);   // every CTA of the cluster has read its start state: the slot may be overwritten
+    if (!PACKED && rank == 0 && warp == 0 && act && p.state_out) run.store(p.state_out + b * C + c0);
 }
 
 template <typename IO, typename SH>
@@ -818,6 +832,7 @@ scan_step_kernel(long long n, const IO *__restrict__ x, const float *__restrict_
 __global__ void __launch_bounds__(256)
 scan_rows_kernel(int T, int padded, int row_blocks, int N, long long C, const int *__restrict__ cu,
                  int *__restrict__ codes, float *__restrict__ zero_state, unsigned *err) {
+    grid_release();
     if ((int)blockIdx.x < row_blocks) {
         const int t = blockIdx.x * 256 + threadIdx.x;
         if (t >= padded) return;
@@ -888,7 +903,7 @@ struct Forward {
             return cudaErrorInvalidValue;
         q.s = scan_params<Forward>(a, K);
         q.err = device_error_word();
-        return launch_cluster<Forward>(q, cols(a), K, a.stream);
+        return launch_cluster<Forward>(q, cols(a), K, a.stream, PACKED);
     }
 };
 
@@ -914,7 +929,7 @@ struct Backward {
             return cudaErrorInvalidValue;
         q.b = backward_params<Backward>(a, K);
         q.err = device_error_word();
-        return launch_cluster<Backward>(q, cols(a), K, a.stream);
+        return launch_cluster<Backward>(q, cols(a), K, a.stream, false);
     }
 };
 

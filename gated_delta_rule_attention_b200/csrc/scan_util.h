@@ -92,23 +92,27 @@ double estimate(long long cols, long long tiles, int K) {
     return waves * ((tiles + K - 1) / K + 1) * (step > fed ? step : fed);
 }
 
+// early: the kernel may start when the one in front of it says so (grid_release), and waits for
+// its results itself (grid_wait).
 template <typename L, typename P>
-cudaError_t launch_cluster(const P &p, long long cols, int K, cudaStream_t stream) {
+cudaError_t launch_cluster(const P &p, long long cols, int K, cudaStream_t stream, bool early) {
     constexpr auto kernel = L::kernel;
     cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::smem(K));
     if (err == cudaSuccess && K > 8) err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (err != cudaSuccess) return err;
     if (cols > INT32_MAX / K) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim = {(unsigned)K, 1, 1};
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3((unsigned)(cols * K));
     cfg.blockDim = dim3(L::kBlock);
     cfg.dynamicSmemBytes = L::smem(K);
     cfg.stream = stream;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = early ? 2 : 1;
     timer_begin(stream);
     err = cudaLaunchKernelEx(&cfg, kernel, p);
     timer_end(stream);
