@@ -843,7 +843,7 @@ def _rotary(q, k, B, T, Hq, Hk, d, freqs, positions, start, scale, flags, yq, yk
     _need(q, q.shape, dt, "q")
     if k is not None:
         _need(k, k.shape, dt, "k")
-    _int32(B=B, T=T, start=start)
+    _int32(B=B, T=T, start=start, d=d, heads=Hq + Hk)
     _need(freqs, (freqs.numel(),), torch.float64, "freqs")
     st = library().la_rotary(dtype, B, T, Hq, Hk, d, 2 * freqs.numel(), _at(q), _at(k), _at(freqs),
                              _at(positions), start, scale, _at(yq), _at(yk), flags, _raw_stream(q, stream))

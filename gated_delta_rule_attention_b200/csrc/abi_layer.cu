@@ -207,6 +207,7 @@ extern "C" la_status_t la_rotary(la_dtype_t dtype, int B, int T, int H_q, int H_
         return LA_ERR_INVALID_ARG;
     if (d > 512) return LA_ERR_UNSUPPORTED;
     const long long most = H_q > H_k ? H_q : H_k;
+    if ((long long)H_q + H_k > (1 << 30)) return LA_ERR_INVALID_ARG;   // the kernel counts heads in 32 bits
     if ((long long)B * T > kMaxElems / (most * d)) return LA_ERR_INVALID_ARG;
     if (T == 0) return LA_OK;
     if (!tensor_ok(freqs, 8) || (positions && !tensor_ok(positions, 4))) return LA_ERR_INVALID_ARG;

@@ -96,8 +96,8 @@ __device__ __forceinline__ void row_sums(float2 (&v)[ROWS], float2 (*box)[NT > 3
 }
 
 // Scale of a group whose largest |y| is `top`: 1 for zeros, and never so small that its
-// reciprocal overflows.  The products with reciprocals instead of quotients leave scale and q
-// within two half steps of fp32, far below a step of e4m3.
+// reciprocal overflows.  The products with reciprocals instead of quotients are off by a few
+// half steps of fp32, far below a step of e4m3.
 __device__ __forceinline__ float fp8_scale(float top) {
     return top > 0.f ? fmaxf(top * (1.f / kFp8Max), 1.17549435e-38f) : 1.f;
 }
@@ -158,7 +158,8 @@ __device__ __forceinline__ Pack<IO, V> row_pack(const void *base, long long at, 
 // loads in flight together, one reduction for all of them).  FP8: 1 a scale a row, 2 a scale for
 // each 128 columns (16 neighbouring lanes).
 template <typename IO, int V, int K, int NT, int ROWS, bool RES, int FP8>
-__global__ void __launch_bounds__(NT <= 32 ? 256 : NT, (RES && ROWS * K * V >= 32 ? 768 : 1024) / (NT <= 32 ? 256 : NT)) norm_kernel(const NormParams p) {
+__global__ void __launch_bounds__(NT <= 32 ? 256 : NT, (RES && ROWS * K * V >= 32 ? 768 : 1024) / (NT <= 32 ? 256 : NT))
+norm_kernel(const NormParams p) {
     constexpr int kBlock = NT <= 32 ? 256 : NT;
     constexpr int kRowsBlock = NT <= 32 ? kBlock / NT : 1;
     static_assert(NT <= 32 || NT == kBlock, "a row has part of a warp, a warp or a CTA");
@@ -442,7 +443,6 @@ cudaError_t launch_forward(const NormArgs &a) {
 
 template <typename IO, int V, int K, int NT, int ROWS>
 cudaError_t forward_kind(const NormArgs &a) {
-    // C > 1024 of vectors comes here by kind; the others take any
     if (!a.fp8)
         return a.residual ? launch_forward<IO, V, K, NT, ROWS, true, 0>(a) : launch_forward<IO, V, K, NT, ROWS, false, 0>(a);
     if constexpr (V == 8 && NT >= 16) {

@@ -390,9 +390,13 @@ la_status_t la_prefill_backward_delta(la_mode_t mode, la_dtype_t dtype, int B, i
  *   checkpoints [B, ceil(T / 32), C] fp32, out, or NULL: the state in front of every 32nd row
  *               (row 0: h_0), for la_linear_scan_backward
  *   flags       LA_FLAG_INIT_STATE | LA_SCAN_BLEND
- * Any C >= 1, and tensors may start at any element (a row of a larger one): C a multiple of 4
- * with 16-byte starts takes four channels a thread, else two or, slowest, one.  T = 0 leaves or
- * zeroes the state.  No output may overlap an input or another output.
+ * Gates are decays: runs of rows are joined by the products of their gates, so gates above 1
+ * whose product over the sequence overflows give infinities or NaN even where the state is 0.
+ * What follows an infinity or a NaN in its channel and sequence is an infinity or NaN.
+ * Any C >= 1, and tensors may start at any element (a row of a larger one): rows that are
+ * multiples of 16 bytes with 16-byte starts come by TMA, others by copies
+ * of single words, two channels a lane where C and the starts are even and, slowest, one.
+ * T = 0 leaves or zeroes the state.  No output may overlap an input or another output.
  */
 la_status_t la_linear_scan(la_dtype_t dtype, int B, int T, int C, const void *x, const float *gate,
                            float *state, void *h, float *checkpoints, unsigned flags, void *stream);

@@ -122,6 +122,8 @@ def test_python_checks(la):
         la.rotary(x, freqs=f, d=8, in_place=True)
     with pytest.raises(ValueError, match="32 bits"):
         la.rotary(x, freqs=f, d=8, start=2 ** 31)
+    with pytest.raises(ValueError, match="heads"):
+        la.rotary(torch.empty(1, 1, 2 ** 33, device="meta"), freqs=f[:1], d=2)
     with pytest.raises(ValueError, match="positions"):
         la.rotary_step(x[0], freqs=f, d=8, positions=torch.zeros(3, dtype=torch.int32))
     with pytest.raises(ValueError, match="group"):
