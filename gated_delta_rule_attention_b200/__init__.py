@@ -693,11 +693,10 @@ def linear_scan(x, gate, *, state=None, init_state: bool | None = None, blend: b
         raise ValueError("init_state needs a state")
     with _on(stream):
         if state is None:
-            state = torch.empty(B, C, device=x.device, dtype=torch.float32)
+            state = x.new_empty((B, C), dtype=torch.float32)
         if h is None:
             h = torch.empty_like(x)
-        kept = (torch.empty(B, -(-T // SCAN_CHECKPOINT), C, device=x.device, dtype=torch.float32)
-                if checkpoints else None)
+        kept = x.new_empty((B, -(-T // SCAN_CHECKPOINT), C), dtype=torch.float32) if checkpoints else None
     _need(state, (B, C), torch.float32, "state")
     _need(h, (B, T, C), dt, "h")
     flags = (FLAG_INIT_STATE if init_state else 0) | (SCAN_BLEND if blend else 0)
@@ -730,10 +729,10 @@ def linear_scan_varlen(x, gate, cu_seqlens, *, state=None, init_state: bool | No
     nbytes = int(library().la_linear_scan_varlen_workspace_size(T))
     with _on(stream):
         if state is None:
-            state = torch.empty(N, C, device=x.device, dtype=torch.float32)
+            state = x.new_empty((N, C), dtype=torch.float32)
         if h is None:
             h = torch.empty_like(x)
-        ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=x.device)
+        ws = x.new_empty(max(nbytes, 16), dtype=torch.uint8)
     _need(state, (N, C), torch.float32, "state")
     _need(h, (T, C), dt, "h")
     flags = (FLAG_INIT_STATE if init_state else 0) | (SCAN_BLEND if blend else 0)
@@ -791,8 +790,8 @@ def linear_scan_backward(x, gate, dh, *, state0=None, checkpoints=None, dstate=N
     with _on(stream):
         dx = torch.empty_like(x)
         dgate = torch.empty_like(gate) if need_dgate else None
-        dstate0 = torch.empty(B, C, device=x.device, dtype=torch.float32) if need_dstate0 else None
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device) if nbytes else None
+        dstate0 = x.new_empty((B, C), dtype=torch.float32) if need_dstate0 else None
+        ws = x.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
     st = library().la_linear_scan_backward(dtype, B, T, C, _at(x), _at(gate), _at(state0), _at(checkpoints),
                                            _at(dh), _at(dstate), _at(dx), _at(dgate), _at(dstate0),
                                            SCAN_BLEND if blend else 0, _at(ws), nbytes,
@@ -879,7 +878,7 @@ def _rotary_rows(q, k, freqs, d, positions, start, scale, flags, y_tokens, in_pl
         yq, yk = q, k
     else:
         def out(H):
-            return torch.empty((B, T, H * d) if y_tokens else (B, H, T, d), device=q.device, dtype=q.dtype)
+            return q.new_empty((B, T, H * d) if y_tokens else (B, H, T, d))
         with _on(stream):
             yq, yk = out(Hq), (None if k is None else out(Hk))
     flags |= (ROT_X_TOKENS if x_tokens else 0) | (ROT_Y_TOKENS if y_tokens else 0)
@@ -912,8 +911,8 @@ def rotary_step(q, k=None, *, freqs, d: int, positions, scale: float = 1.0, inte
         raise ValueError("d must divide the last dimension of q and k")
     _need(positions, (N,), torch.int32, "positions")
     with _on(stream):
-        yq = torch.empty((N, Cq // d, d), device=q.device, dtype=q.dtype)
-        yk = None if k is None else torch.empty((N, Ck // d, d), device=q.device, dtype=q.dtype)
+        yq = q.new_empty((N, Cq // d, d))
+        yk = None if k is None else q.new_empty((N, Ck // d, d))
     # a token's rows [H*d] are its head rows [H, 1, d]
     return _rotary(q, k, N, 1, Cq // d, Ck // d, d, freqs, positions, 0, float(scale),
                    (ROT_INTERLEAVED if interleaved else 0) | ROT_X_TOKENS, yq, yk, stream)
@@ -942,8 +941,9 @@ def _rms_norm(x, B, H, T, C, w, residual, residual_out, eps, fp8, group, y_shape
         raise ValueError("residual_out needs residual")
     _int32(B=B, H=H, rows=T, C=C)
     with _on(stream):
-        y = torch.empty(y_shape, device=x.device, dtype=torch.float8_e4m3fn if fp8 else dt)
-        scales = torch.empty(scale_shape, device=x.device, dtype=torch.float32) if fp8 else None
+        ydt = torch.float8_e4m3fn if fp8 else dt
+        y = torch.empty_like(x, dtype=ydt) if y_shape is None else x.new_empty(y_shape, dtype=ydt)
+        scales = x.new_empty(scale_shape, dtype=torch.float32) if fp8 else None
         if residual is not None and residual_out is None:
             residual_out = torch.empty_like(x)
     if residual is not None:
@@ -976,8 +976,8 @@ def rms_norm(x, w, *, residual=None, residual_out=None, eps: float = 1e-6, fp8: 
     C = x.shape[-1]
     if group and C % group:
         raise ValueError("group must divide the last dimension")
-    return _rms_norm(x, 1, 1, _rows(x), C, w, residual, residual_out, eps, fp8, group, x.shape,
-                     (*x.shape[:-1], C // group if group else 1), stream)
+    return _rms_norm(x, 1, 1, _rows(x), C, w, residual, residual_out, eps, fp8, group, None,
+                     (*x.shape[:-1], C // group if group else 1) if fp8 else None, stream)
 
 
 def rms_norm_heads(x, w, *, eps: float = 1e-6, fp8: bool = False, stream=None):
@@ -1000,7 +1000,7 @@ def _rms_norm_backward(h, B, H, T, C, w, dy, dy_shape, dresidual, eps, stream):
     nbytes = int(library().la_rms_norm_backward_workspace_size(B, H, T, C))
     with _on(stream):
         dx, dw = torch.empty_like(h), torch.empty_like(w)
-        ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=h.device)
+        ws = h.new_empty(max(nbytes, 16), dtype=torch.uint8)
     st = library().la_rms_norm_backward(dtype, B, H, T, C, _at(h), _at(w), float(eps), _at(dy),
                                         _at(dresidual), _at(dx), _at(dw), _at(ws), ws.numel(),
                                         _raw_stream(h, stream))
