@@ -35,11 +35,11 @@
 // on chip.
 //
 // What bounds it: HBM where there are columns for every SM: forward B2 T32768 C2048 bf16, 128
-// CTAs of 32 channels, 168 us, 97 % of the copy rate (a first version with lanes copying their
-// own values, shuffles and a cluster barrier a step took 444).  A CTA's step is a chain of
-// latencies (barrier, shared-memory reads, fold: 1.0 to 1.3 us a tile), so with few columns the
-// time axis goes over K CTAs and walk 1 of the next step comes before walk 2 of this one (AHEAD):
-// the runs travel meanwhile (B1 T50001 C192 fp32: 32 us, floor 18; 42 without AHEAD).
+// CTAs of 32 channels, 157 to 167 us, 98 % of the copy rate and more (a first version with lanes copying
+// their own values, shuffles and a cluster barrier a step took 444); backward 315 us, 91 %.  A CTA's
+// step is a chain of latencies (barrier, shared-memory reads, fold: 1.0 to 1.3 us a tile), so with
+// few columns the time axis goes over K CTAs and walk 1 of the next step comes before walk 2 of this
+// one (AHEAD): the runs travel meanwhile (B1 T50001 C192 fp32: 28 us, floor 18; 42 without AHEAD).
 #include "scan_util.h"
 #include "tmap.cuh"
 
@@ -322,10 +322,29 @@ __device__ __forceinline__ Lane<V> meet(Exchange<V, STAGES> *ex, const Run<V> *s
     const int lane = threadIdx.x & 31, slot = step % kSlots;
     ptx::mbar_wait(&ex->met[slot], (step / kSlots) & 1, &ex->abort, err);
     Lane<V> in = run;
-    for (int r = 0; r < K; ++r) {
-        if (r == rank) in = run;
-        const Run<V> e = slots[((size_t)slot * K + r) * 32 + lane];
-        run = (RESETS && ex->slot_reset[slot][r]) ? e.H : fma(e.P, run, e.H);
+    // loads in flight together: all of the few, else four (B1 T20011 C1024 bf16 33.4 us; 34.7 one after
+    // the other, 35 all sixteen)
+    auto join = [&](int r0, auto ranks) {
+        constexpr int N = decltype(ranks)::value;
+        Run<V> e[N];
+        int reset[N];
+        const Run<V> *from = slots + ((size_t)slot * K + r0) * 32 + lane;
+#pragma unroll
+        for (int r = 0; r < N; ++r) {
+            e[r] = from[r * 32];
+            reset[r] = RESETS ? ex->slot_reset[slot][r0 + r] : 0;
+        }
+#pragma unroll
+        for (int r = 0; r < N; ++r) {
+            if (r0 + r == rank) in = run;
+            run = reset[r] ? e[r].H : fma(e[r].P, run, e[r].H);
+        }
+    };
+    if (K == 2) {
+        join(0, std::integral_constant<int, 2>{});
+    } else {
+#pragma unroll 1
+        for (int r0 = 0; r0 < K; r0 += 4) join(r0, std::integral_constant<int, 4>{});
     }
     return in;
 }
@@ -399,9 +418,9 @@ __global__ void __launch_bounds__(kThreads, AHEAD ? 1 : 2) scan_kernel(const __g
             if (PACKED && step >= STAGES) ptx::bulk_load(to + St::kGate + St::kX, p.codes + t0, TT * 4, bar);
         }
     };
-    // A packed call's kernel starts while scan_rows_kernel still runs (which itself waits for all
-    // that is in front of it in the stream), asks for the first rows, and waits for the codes:
-    // 61 sequences, T20011 C1024 bf16, 51 us instead of 54.
+    // A packed call's kernel (AHEAD) starts while scan_rows_kernel still runs (which itself waits for
+    // all that is in front of it in the stream), asks for the first rows, and waits for the codes: 61
+    // sequences, T20011 C1024 bf16, 1 us of 45.
     if (PACKED && !TMA) grid_wait();
     for (int i = 0; i < STAGES; ++i) fetch(i);
     if (PACKED && TMA && asks == 1) {
@@ -903,7 +922,9 @@ struct Forward {
             return cudaErrorInvalidValue;
         q.s = scan_params<Forward>(a, K);
         q.err = device_error_word();
-        return launch_cluster<Forward>(q, cols(a), K, a.stream, PACKED);
+        // two CTAs an SM would be placed unevenly around scan_rows_kernel's blocks (one sequence after
+        // the other, T8192 C4096 fp32: 86 us, 72 when they wait for its end)
+        return launch_cluster<Forward>(q, cols(a), K, a.stream, PACKED && AHEAD);
     }
 };
 
