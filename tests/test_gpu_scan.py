@@ -230,6 +230,46 @@ def test_scan_varlen_many_sequences_in_place(la):
     close(h, rh, b)
 
 
+@pytest.mark.parametrize("C", [192, 1024, 101])
+def test_scan_varlen_sees_what_the_stream_wrote(la, C):
+    """Inputs, offsets and states written by kernels right in front of the call, in turn, with nothing
+    waited for in between: the same bits as of calls by themselves."""
+    T, N, kinds = 6000, 37, 3
+    g = torch.Generator().manual_seed(C)
+    given, want = [], []
+    for i in range(kinds):
+        x, gate, _ = inputs(torch.bfloat16, T, C, seed=C + i)
+        cuts = torch.randint(0, T + 1, (N - 1,), generator=g).sort().values.tolist()
+        cu = torch.tensor([0, *cuts, T], dtype=torch.int32, device="cuda")
+        given.append((x, gate, cu, torch.randn(N, C, device="cuda")))
+        state = given[i][3].clone()
+        torch.cuda.synchronize()
+        want.append((la.linear_scan_varlen(x, gate, cu, state=state)[0], state))
+        torch.cuda.synchronize()
+    x, gate, cu, state = (torch.empty_like(t) for t in given[0])
+    got = []
+    for i in range(30):
+        for to, t in zip((x, gate, cu, state), given[i % kinds]):
+            to.copy_(t)
+        h, _ = la.linear_scan_varlen(x, gate, cu, state=state)
+        got.append((h, state.clone()))
+    la.check_status()
+    for i, (h, last) in enumerate(got):
+        assert torch.equal(h, want[i % kinds][0]) and torch.equal(last, want[i % kinds][1]), i
+
+
+def test_scan_state_in_place_over_clusters(la):
+    """The state read and written in place by calls that split the time over a cluster."""
+    x, gate, _ = inputs(torch.float32, 2, 700, 64, seed=21)
+    h0 = torch.randn(2, 64, device="cuda")
+    want, end = la.linear_scan(x, gate, state=h0.clone())
+    for _ in range(50):
+        state = h0.clone()
+        h, _ = la.linear_scan(x, gate, state=state)
+        assert torch.equal(h, want) and torch.equal(state, end)
+    la.check_status()
+
+
 def test_scan_varlen_bad_offsets_are_reported(la):
     x, gate, _ = inputs(torch.bfloat16, 100, 64, seed=1)
     for bad in ([0, 60, 40, 500], [-5, 50, 100, 100], [0, 200, 300, 400]):
