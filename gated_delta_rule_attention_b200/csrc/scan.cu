@@ -990,7 +990,7 @@ bool rows_by_tma(const ScanBackwardArgs &a) {
 // The variants, of which a call takes the one with the least estimated time:
 //   two CTAs an SM, K = 1, a step after the other: many columns;
 //   one CTA an SM, AHEAD, K = 1 .. 16: few columns, and with a ring of 144 KB and more also the
-//   fastest where 32-channel columns fill the SMs once (B2 T32768 C2048 bf16: 167 us against 172).
+//   fastest where 32-channel columns fill the SMs once (B2 T32768 C2048 bf16: 157 us against 168).
 // V = 2 has half the columns and 256-byte gate rows, V = 1 twice the CTAs.
 // Rows that TMA cannot take are bound by their lanes' copies, two channels at a time where C and
 // the starts are even (B2 T5000 C1002 bf16 28 us, floor 12), else one (C1001 40 us).
